@@ -12,13 +12,19 @@ Entry points mirror include/attn.h:
     attn_decode_multi(q, k_cache, v_cache, seqlens, ...)
     attn_bwd(q, k, v, o, lse, dout, ...)
     key_stats(k), attn_fwd_bound(q, k, v, kbar, radius, ...)
+    rope(q, k, positions, axes, freq, ...)
+    kv4_pool(...), kv4_append(k, v, pool, table, seqlens, ...), kv4_read(...)
+    attn_decode_kv4(q, pool, table, seqlens, ...)
+    copy_pages(pool, src, dst)
     frame_block_map(n_frames, frame_len)
     classify(mask_kind, block_map, Nq, Nkv, tq, tk)
     plan(mask_kind, block_map, Nq, Nkv)
     sync_status(stream=None)
 
 Above these: exact_io_aware_sm_b200.autograd.attention (the differentiable op,
-attn_fwd forward and attn_bwd backward) and exact_io_aware_sm_b200.ulysses
+attn_fwd forward and attn_bwd backward; rope there is differentiable too),
+exact_io_aware_sm_b200.kv4_cache (the pages of a 4-bit cache: sequences added,
+extended, forked, freed and compacted) and exact_io_aware_sm_b200.ulysses
 (sequence-parallel forward, backward and differentiable op over
 torch.distributed).
 
@@ -29,6 +35,7 @@ being written or read past its end.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -77,9 +84,18 @@ def lib() -> ctypes.CDLL:
         L.attn_debug_fault.argtypes = [I]
         L.attn_key_stats.argtypes = [P, P, P, I, I, I, I, P]
         L.attn_fwd_bound.argtypes = [P, P, P, P, P, I, I, I, I, I, I, F, I, P, P, P, P, P]
+        D = ctypes.c_int64
+        L.attn_rope.argtypes = [P] * 8 + [I] * 10 + [P]
+        L.attn_kv4_append.argtypes = [P] * 7 + [I] * 7 + [P]
+        L.attn_kv4_read.argtypes = [P] * 6 + [I] * 7 + [P]
+        L.attn_decode_kv4.argtypes = [P] * 7 + [D] + [I] * 8 + [F, P]
+        L.attn_decode_kv4_workspace.argtypes = [I] * 7
+        L.attn_decode_kv4_workspace.restype = D
+        L.attn_copy_pages.argtypes = [P, D, I, P, P, I, P]
         L.attn_version.restype = ctypes.c_char_p
         for fn in (L.attn_fwd, L.attn_decode, L.attn_decode_multi, L.attn_bwd, L.attn_frame_block_map,
-                   L.attn_classify, L.attn_plan, L.attn_key_stats, L.attn_fwd_bound,
+                   L.attn_classify, L.attn_plan, L.attn_key_stats, L.attn_fwd_bound, L.attn_rope,
+                   L.attn_kv4_append, L.attn_kv4_read, L.attn_decode_kv4, L.attn_copy_pages,
                    L.attn_sync_status, L.attn_last_error_detail, L.attn_shutdown, L.attn_debug_fault):
             fn.restype = I
         _lib = L
@@ -277,6 +293,247 @@ def attn_decode_multi(q, k_cache, v_cache, seqlens, o=None, lse=None, scale=None
                                    o.data_ptr(), None if lse is None else lse.data_ptr(), B, Sq, Hq, Hkv,
                                    Lmax, d, float(scale), _stream_ptr(stream)))
     return o, lse
+
+
+def _on(stream):
+    """The context that allocates a call's outputs and workspace on the stream that
+    the call runs on (so that their memory is not reused while it runs)."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device_index != torch.cuda.current_device():
+        raise ValueError(f"stream is on device {stream.device_index} but the current CUDA device is "
+                         f"{torch.cuda.current_device()}")
+    return torch.cuda.stream(stream)
+
+
+def _need_rows(t, name, shape, dtype, device=None):
+    """_need for a [B, N, H, d] tensor whose heads and channels are contiguous but whose
+    batch and token strides are free (a part of a fused projection); returns those two
+    strides (0 for dimensions of one element)."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected 4 dimensions")
+    B, N, H, d = t.shape
+    sb, sn, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d):
+        raise ValueError(f"{name} must have contiguous heads and channels (strides {t.stride()})")
+    if t.numel():
+        _need(t[:1, :1], name, (1, 1, H, d), (dtype,), device)
+    if any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple('*' if w is None else w for w in shape)}")
+    return (sb if B > 1 else 0), (sn if N > 1 else 0)
+
+
+def _extent(t):
+    """First and one-past-last byte address of a tensor's elements."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _apart(out, name, others):
+    """Refuse an output [B,N,H,d] that repeats its own rows, or that overlaps one of
+    `others` (tensor, may it be that very tensor).  Rows of one fused buffer, side by side
+    at the same strides, do not overlap."""
+    B, N, H, d = out.shape
+    e, row = out.element_size(), H * d
+    dims = sorted((s, n) for s, n in ((out.stride(0), B), (out.stride(1), N)) if n > 1)
+    span = row
+    for s, n in dims:
+        if s < span:
+            raise ValueError(f"{name} must not repeat elements (strides {out.stride()})")
+        span = (n - 1) * s + span
+    lo, hi = _extent(out)
+    for t, same in others:
+        if same and t.data_ptr() == out.data_ptr() and t.shape == out.shape and t.stride() == out.stride():
+            continue
+        a, b = _extent(t)
+        if a >= hi or lo >= b:
+            continue
+        if dims and t.dim() == 4 and t.shape[:2] == out.shape[:2] and t.stride()[:2] == out.stride()[:2]:
+            step = dims[0][0] * e
+            r = (a - lo) % step
+            if all(s * e % step == 0 for s, _ in dims) and r >= row * e and step - r >= t.shape[2] * d * e:
+                continue
+        raise ValueError(f"{name} overlaps another tensor of the call")
+
+
+def rope(q, k, positions, axes, freq, interleaved=False, inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotary positions with several axes.  q [B,N,Hq,d], k [B,N,Hk,d] (or None), bf16 or
+    fp32; positions int32 [B,N,A] (or [N,A] for every sequence); axes and freq: host
+    arrays of n <= d/2 entries, pair p turning by positions[..., axes[p]] * freq[p].
+    Pair p is channels (p, p + d/2), or (2p, 2p + 1) if interleaved; channels without an
+    entry are copied.  inverse rotates back.  q and k may have any batch and token
+    strides of whole 16 bytes; q_out may be q, and k_out k.  Returns (q_out, k_out)."""
+    import torch
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q has dtype {q.dtype}; expected torch.bfloat16 or torch.float32")
+    qs = _need_rows(q, "q", (None,) * 4, q.dtype)
+    B, N, Hq, d = q.shape
+    ks, Hk = (0, 0), 0
+    if k is not None:
+        ks = _need_rows(k, "k", (B, N, None, d), q.dtype, q.device)
+        Hk = k.shape[2]
+    axes = np.ascontiguousarray(axes, dtype=np.uint8)
+    freq = np.ascontiguousarray(freq, dtype=np.float64)
+    if axes.ndim != 1 or axes.shape != freq.shape:
+        raise ValueError(f"axes and freq must be vectors of one length, got {axes.shape} and {freq.shape}")
+    if positions.dim() == 2:
+        positions = positions.expand(B, *positions.shape)
+    if positions.dim() != 3 or tuple(positions.shape[:2]) != (B, N):
+        raise ValueError(f"positions has shape {tuple(positions.shape)}; expected ({B}, {N}, *) or ({N}, *)")
+    A = positions.shape[2]
+    if A > 1 and positions.stride(2) != 1:
+        raise ValueError("positions must be contiguous in its last dimension")
+    if positions.numel():
+        _need(positions[:1, :1], "positions", (1, 1, A), (torch.int32,), q.device)
+    ps = (positions.stride(0) if B > 1 else 0), (positions.stride(1) if N > 1 else 0)
+    with _on(stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _apart(q_out, "q_out", [(q, True), (positions, False)] + ([(k, False)] if k is not None else []))
+        if k_out is None and k is not None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        elif k is not None:
+            _apart(k_out, "k_out", [(k, True), (q, False), (q_out, False), (positions, False)])
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+    qo = _need_rows(q_out, "q_out", q.shape, q.dtype, q.device)
+    ko = _need_rows(k_out, "k_out", k.shape, q.dtype, q.device) if k is not None else (0, 0)
+    if q.numel() == 0 or (k is not None and k.numel() == 0):
+        raise ValueError(f"q and k must not be empty, got {tuple(q.shape)}" + (f" and {tuple(k.shape)}" if k is not None else ""))
+    strides = (ctypes.c_int64 * 10)(*qs, *ks, *qo, *ko, *ps)
+    _check(lib().attn_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                           None if k is None else k_out.data_ptr(), positions.data_ptr(), _np_ptr(axes),
+                           _np_ptr(freq), strides, B, N, Hq, Hk, d, A, len(axes), int(interleaved), int(inverse),
+                           BF16 if q.dtype == torch.bfloat16 else F32, _stream_ptr(stream)))
+    return q_out, k_out
+
+
+KV4_GROUP = 32  # channels that share a scale
+
+
+def kv4_page_bytes(page, Hkv, d):
+    """Bytes of a page of `page` tokens (16, 32, 64, 128 or 256): K and V codes and scales of every KV head."""
+    if page not in (16, 32, 64, 128, 256) or d not in (64, 128):
+        raise ValueError(f"page must be 16, 32, 64, 128 or 256 (got {page}) and d 64 or 128 (got {d})")
+    return page // 16 * 18 * d * Hkv
+
+
+def kv4_pool(n_pages, Hkv, d, page=64, device=None):
+    """An empty pool of a 4-bit cache: uint8 [n_pages, Hkv, page/16 * 18 d] (uninitialised)."""
+    import torch
+    return torch.empty((n_pages, Hkv, kv4_page_bytes(page, 1, d)), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def _kv4(pool, table, seqlens, B, Hkv, d, device):
+    """Check a pool, page table and lengths; returns (n_pages, Hkv, page, max_pages)."""
+    import torch
+    _need(pool, "pool", (None, Hkv, None), (torch.uint8,), device)
+    _need(table, "table", (B, None), (torch.int32,), pool.device)
+    _need(seqlens, "seqlens", (table.shape[0],), (torch.int32,), pool.device)
+    n_pages, heads, nbytes = pool.shape
+    if d not in (64, 128):
+        raise ValueError(f"the 4-bit cache needs d in (64, 128), got {d}")
+    page = nbytes // (18 * d) * 16
+    if page not in (16, 32, 64, 128, 256) or nbytes != page // 16 * 18 * d:
+        raise ValueError(f"pool has {nbytes} bytes a page and head: no page of 16, 32, 64, 128 or 256 tokens at d = {d}")
+    return n_pages, heads, page, table.shape[1]
+
+
+def kv4_append(k, v, pool, table, seqlens, n_new=None, stream=None):
+    """Quantise k, v [B,N,Hkv,d] bf16 (any batch and token strides of whole 16 bytes) and
+    write them into the pages of pool (kv4_pool) that table int32 [B,max_pages] names, as
+    tokens seqlens[b] - n_new[b] .. seqlens[b] - 1; n_new int32 [B] (None: N each), rows
+    behind it are padding.  Nothing else in the pool changes.  Returns pool."""
+    import torch
+    ks = _need_rows(k, "k", (None,) * 4, torch.bfloat16)
+    B, N, Hkv, d = k.shape
+    vs = _need_rows(v, "v", k.shape, torch.bfloat16, k.device)
+    n_pages, _, page, max_pages = _kv4(pool, table, seqlens, B, Hkv, d, k.device)
+    if n_new is not None:
+        _need(n_new, "n_new", (B,), (torch.int32,), k.device)
+    with _on(stream):
+        strides = (ctypes.c_int64 * 4)(*ks, *vs)
+        _check(lib().attn_kv4_append(k.data_ptr(), v.data_ptr(), pool.data_ptr(), table.data_ptr(),
+                                     seqlens.data_ptr(), None if n_new is None else n_new.data_ptr(), strides, B, N,
+                                     Hkv, d, n_pages, page, max_pages, _stream_ptr(stream)))
+    return pool
+
+
+def kv4_read(pool, table, seqlens, N, d, start=None, k=None, v=None, stream=None):
+    """Tokens start[b] .. start[b] + N - 1 (start int32 [B]; None: 0) of each sequence of a
+    4-bit cache as bf16 k, v [B,N,Hkv,d]; rows at and past seqlens[b] are zeros."""
+    import torch
+    n_pages, Hkv, page, max_pages = _kv4(pool, table, seqlens, None, None, d, None)
+    B = table.shape[0]
+    if start is not None:
+        _need(start, "start", (B,), (torch.int32,), pool.device)
+    with _on(stream):
+        if k is None:
+            k = torch.empty((B, N, Hkv, d), dtype=torch.bfloat16, device=pool.device)
+        if v is None:
+            v = torch.empty((B, N, Hkv, d), dtype=torch.bfloat16, device=pool.device)
+        _need(k, "k", (B, N, Hkv, d), (torch.bfloat16,), pool.device)
+        _need(v, "v", (B, N, Hkv, d), (torch.bfloat16,), pool.device)
+        _check(lib().attn_kv4_read(k.data_ptr(), v.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(),
+                                   None if start is None else start.data_ptr(), B, N, Hkv, d, n_pages, page,
+                                   max_pages, _stream_ptr(stream)))
+    return k, v
+
+
+def attn_decode_kv4(q, pool, table, seqlens, o=None, lse=None, scale=None, stream=None, want_lse=True):
+    """Decode of the Sq newest tokens per sequence over a 4-bit paged cache.  q
+    [B,Sq,Hq,d] bf16; pool from kv4_pool; table int32 [B,max_pages]; seqlens int32 [B]
+    on the device (including the Sq new tokens).  Returns o [B,Sq,Hq,d] and lse [B,Hq,Sq]."""
+    import torch
+    _need(q, "q", (None,) * 4, (torch.bfloat16,))
+    B, Sq, Hq, d = q.shape
+    n_pages, Hkv, page, max_pages = _kv4(pool, table, seqlens, B, None, d, q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    L = lib()
+    with _on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _need(o, "o", q.shape, (torch.bfloat16,), q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        elif lse is not None:
+            _need(lse, "lse", (B, Hq, Sq), (torch.float32,), q.device)
+        n = L.attn_decode_kv4_workspace(B, Sq, Hq, Hkv, d, page, max_pages)
+        work = torch.empty(n, dtype=torch.uint8, device=q.device) if n > 0 else None
+        _check(L.attn_decode_kv4(q.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
+                                 None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(),
+                                 max(n, 0), B, Sq, Hq, Hkv, d, n_pages, page, max_pages, float(scale),
+                                 _stream_ptr(stream)))
+    return o, lse
+
+
+def copy_pages(pool, src, dst, stream=None):
+    """Copy pages src[i] of a pool to pages dst[i].  pool: a contiguous CUDA tensor of
+    equal pages along its first dimension; src, dst: host int arrays.  A source may
+    repeat; no page may be a destination twice, or source and destination.  Returns pool."""
+    if not getattr(pool, "is_cuda", False) or pool.dim() < 1 or not len(pool):
+        raise ValueError("pool must be a CUDA tensor of at least one page")
+    _need(pool, "pool", (None,) * pool.dim(), (pool.dtype,))
+    src, dst = np.asarray(src), np.asarray(dst)
+    if src.ndim != 1 or src.shape != dst.shape:
+        raise ValueError(f"src and dst must be vectors of one length, got {src.shape} and {dst.shape}")
+    if len(src) and not (np.issubdtype(src.dtype, np.integer) and np.issubdtype(dst.dtype, np.integer)):
+        raise ValueError(f"src and dst must hold integers, got {src.dtype} and {dst.dtype}")
+    for name, x in (("src", src), ("dst", dst)):
+        if x.dtype != np.int32 and len(x) and (x.min() < 0 or x.max() >= len(pool)):
+            raise ValueError(f"{name} names a page outside the pool of {len(pool)} pages")
+    src, dst = np.ascontiguousarray(src, dtype=np.int32), np.ascontiguousarray(dst, dtype=np.int32)
+    with _on(stream):
+        _check(lib().attn_copy_pages(pool.data_ptr(), pool.numel() // len(pool) * pool.element_size(), len(pool),
+                                     _np_ptr(src), _np_ptr(dst), len(src), _stream_ptr(stream)))
+    return pool
 
 
 def attn_bwd(q, k, v, o, lse, dout, scale=None, mask_kind=MASK_NONE, block_map=None, stream=None):

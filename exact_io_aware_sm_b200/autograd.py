@@ -1,4 +1,7 @@
-"""Attention as a differentiable PyTorch op: attn_fwd forward, attn_bwd backward.
+"""Attention and rotary positions as differentiable PyTorch ops.
+
+attention: attn_fwd forward, attn_bwd backward.  rope: eio.rope both ways (the
+gradient of a rotation is the rotation back, which keeps nothing but the positions).
 
 The forward keeps only what "FlashAttention: memory-saving exact attention"
 (section 4) says a backward needs: the output O and the row statistics (the
@@ -15,6 +18,8 @@ check this wrapper's bookkeeping against the oracle on the CPU.
 from __future__ import annotations
 
 import math
+
+import numpy as np
 
 
 def default_fwd(q, k, v, mask_kind, scale, block_map):
@@ -64,3 +69,58 @@ def attention(q, k, v, mask_kind=0, scale=None, block_map=None, return_lse=False
         scale = 1.0 / math.sqrt(q.shape[-1])
     o, lse = _FN.apply(q, k, v, mask_kind, float(scale), block_map, fwd or default_fwd, bwd or default_bwd)
     return (o, lse) if return_lse else o
+
+
+def default_rope(q, k, positions, axes, freq, interleaved, inverse):
+    from . import rope as call
+    return call(q, k, positions, axes, freq, interleaved=interleaved, inverse=inverse)
+
+
+def _rows(x):
+    """x, or a contiguous copy where its layout is not one that eio.rope reads (expanded
+    gradients, transposed heads, strides that are not whole 16 bytes)."""
+    B, N, H, d = x.shape
+    e = x.element_size()
+    sb, sn, sh, sd = x.stride()
+    ok = (sd == 1 and (H == 1 or sh == d) and (B == 1 or (sb > 0 and sb * e % 16 == 0))
+          and (N == 1 or (sn > 0 and sn * e % 16 == 0)) and x.data_ptr() % 16 == 0)
+    return x if ok else x.contiguous()
+
+
+def _rope_function():
+    import torch
+
+    class _Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, axes, freq, interleaved, inverse, call):
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(positions)
+            ctx.table = axes, freq, interleaved
+            ctx.inverse, ctx.call = inverse, call
+            yq, yk = call(_rows(q), None if k is None else _rows(k), positions, axes, freq, interleaved, inverse)
+            return yq, yk
+
+        @staticmethod
+        def backward(ctx, dq, dk):
+            positions, = ctx.saved_tensors
+            rest = (positions, *ctx.table, not ctx.inverse, ctx.call)
+            if dq is None:  # only k's output was used
+                gq, gk = None, (None if dk is None else _Rope.apply(dk, None, *rest)[0])
+            else:
+                gq, gk = _Rope.apply(dq, dk, *rest)
+            return gq, gk, None, None, None, None, None, None
+
+    return _Rope
+
+
+_ROPE_FN = None
+
+
+def rope(q, k, positions, axes, freq, interleaved=False, call=None):
+    """eio.rope, differentiable in q and k (any number of times).  Returns (q, k) rotated.
+    `call` replaces the library call, with the signature of default_rope."""
+    global _ROPE_FN
+    if _ROPE_FN is None:
+        _ROPE_FN = _rope_function()
+    axes, freq = np.array(axes, dtype=np.uint8), np.array(freq, dtype=np.float64)  # the backward's own copy
+    return _ROPE_FN.apply(q, k, positions, axes, freq, interleaved, False, call or default_rope)

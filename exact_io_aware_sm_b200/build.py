@@ -17,8 +17,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libattn_b200.so")
 SOURCES = ["api.cu", "plan.cpp", "prefill_sm100.cu", "prefill_f32.cu", "decode.cu", "decode_noalloc.cu",
-           "backward.cu", "key_stats.cu"]
-HEADERS = ["kernels.h", "plan.h", "ptx_sm100.cuh", "pdl.cuh", "warp_mma.cuh", "fastmath.cuh", os.path.join("..", "..", "include", "attn.h")]
+           "backward.cu", "key_stats.cu", "api_kv4.cu", "rope.cu", "kv4_rows.cu", "decode_kv4.cu", "copy_pages.cu"]
+HEADERS = ["kernels.h", "plan.h", "ptx_sm100.cuh", "pdl.cuh", "warp_mma.cuh", "fastmath.cuh", "kv4.cuh",
+           os.path.join("..", "..", "include", "attn.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -340,6 +340,25 @@ void eio::set_error_detail(const char* msg) { std::snprintf(g_err, sizeof g_err,
 
 int eio::require_sm100() { return check_device_sm100(); }
 
+int eio::device_error_word(cudaStream_t s, int** out) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_err(e, "cudaGetDevice");
+  const auto it = g_ws.find(dev);
+  if (it == g_ws.end() || !it->second.d_err) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(s, &st);
+    if (e != cudaSuccess) return cuda_err(e, "cudaStreamIsCapturing");
+    if (st != cudaStreamCaptureStatusNone)
+      return set_err(ATTN_ERR_WORKSPACE, "the first call on a device allocates its error word: make it before a capture");
+  }
+  DevWs* ws;
+  if (int rc = get_ws(&ws)) return rc;
+  *out = ws->d_err;
+  return ATTN_OK;
+}
+
 bool eio::encode_bf16_map(CUtensorMap* m, const void* base, int B, int N, int H, int d, int box_rows) {
   const CUresult r = encode_map(m, base, B, N, H, d, box_rows);
   if (r != CUDA_SUCCESS) {
@@ -710,7 +729,7 @@ int attn_sync_status(void* stream) {
   if (h == 0) return ATTN_OK;
   cudaMemset(ws->d_err, 0, sizeof(int));
   if (h == ATTN_ERR_DEVICE_TIMEOUT) return set_err(h, "a kernel's bounded wait ran out");
-  if (h == ATTN_ERR_DEVICE_ARG) return set_err(h, "a seqlens entry was outside [0, Lmax]");
+  if (h == ATTN_ERR_DEVICE_ARG) return set_err(h, "a seqlens entry was outside [0, Lmax], or an entry of a 4-bit cache call (seqlens, n_new, start, page table) out of range");
   return set_err(h, "device error %d", h);
 }
 

@@ -1,0 +1,81 @@
+// kv4.cuh -- the pages of the 4-bit KV cache: their layout, and the quantiser.
+//
+// A page holds T tokens (16, 32, 64, 128 or 256) of every KV head: [Hkv][T / 16
+// tiles].  A tile is 16 tokens of one head, 18 d bytes, everything that the
+// attention over those 16 keys needs in one contiguous run (a multiple of 128
+// bytes, so that one bulk copy brings any number of consecutive tiles of a page):
+//
+//   K codes   [tok][t 0..3][group][4 bytes]                  8 d bytes
+//   V codes   [tok / 8][g 0..7][t 0..3][group][tok % 2][2 bytes], t = tok % 8 / 2
+//   K scales  [tok][group] bf16                              32 (d / 32) bytes
+//   V scales  [tok][group] bf16
+//
+// A group is 32 channels of one token and head; a code c in 0..15 (4 bits, low
+// nibble first) stands for (c - 8) * s with the group's scale s.  K's channel
+// 32 group + 8 t + n is nibble n of its four bytes; V's channel 32 group + 4 g
+// + i is nibble i of its two.  The orders inside K and V are those of the
+// m16n8k16 fragments that the decode kernel builds from them: lane (g, t) of a
+// warp finds the codes that its A fragments take (K: token g, every group's
+// t-th eight channels; V: tokens 2t, 2t + 1, every group's g-th four channels)
+// in 16 (d = 64: 8) consecutive bytes, and the 32 lanes' runs are consecutive.
+// Every byte belongs to one token, so that a token is written without reading
+// its neighbours.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+
+namespace eio {
+
+constexpr int kKv4Tile = 16;    // tokens
+constexpr int kKv4Group = 32;   // channels that share a scale
+
+__host__ __device__ constexpr int kv4_tile_bytes(int d) { return 18 * d; }
+__host__ __device__ constexpr int kv4_off_v(int d) { return 8 * d; }
+__host__ __device__ constexpr int kv4_off_ks(int d) { return 16 * d; }
+__host__ __device__ constexpr int kv4_off_vs(int d) { return 17 * d; }
+
+// The byte offset of the tile that holds token `tok` of sequence b, head h;
+// -1 (and the error latched) where the table names no page of the pool.
+template <int D>
+__device__ __forceinline__ long long kv4_tile_at(const Kv4Pages& p, int b, int h, int tok, int err_code) {
+  const int id = p.table[static_cast<size_t>(b) * p.max_pages + (tok >> p.page_shift)];
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.n_pages)) {
+    atomicCAS(p.err, 0, err_code);
+    return -1;
+  }
+  const int tiles = 1 << (p.page_shift - 4);
+  return ((static_cast<long long>(id) * p.Hkv + h) * tiles + ((tok >> 4) & (tiles - 1))) * kv4_tile_bytes(D);
+}
+
+// The scale of a group from the largest magnitude of its bf16 values, given
+// as bits (sign cleared; integers order like the magnitudes, infinities and
+// NaNs above all): bf16(m / 7); 0 below 2^-100, so that every scale and its
+// reciprocal are normal fp32 numbers; NaN where the group holds an infinity
+// or a NaN.  m * (1/7) in fp32 rounds to the bf16 of the exact quotient: m
+// has 8 significant bits, so m / 7 is a bf16 value or at least 2^-12 of its
+// size away from every border between two.
+__device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t m) {
+  if (m >= 0x7f80u) return 0x7fffu;
+  if (m < 0x0d80u) return 0u;  // 2^-100
+  const float s = __uint_as_float(m << 16) * (1.f / 7.f);
+  return __bfloat16_as_ushort(__float2bfloat16_rn(s));
+}
+
+// Codes are 8 + floor(x / s + 1/2): x / s has a distance of 0 or at least 2^-9
+// from every half-integer (quotients of two 8-bit significands of magnitude at
+// most 7), so x * (1 / s) + 2^-14 rounded to the nearest integer is that floor
+// whatever the last bits of the product.  The addition of 1.5 * 2^23 + 8 rounds
+// and leaves 8 + the integer in the low bits.  Codes stay in 1..15: |x| is at most m
+// and s at least (m / 7) (1 - 2^-8).  inv is 0 for scales 0 and NaN: code 8.
+__device__ __forceinline__ float kv4_inverse(uint32_t scale_bits) {
+  return scale_bits == 0u || scale_bits >= 0x7f80u ? 0.f : 1.f / __uint_as_float(scale_bits << 16);
+}
+__device__ __forceinline__ uint32_t kv4_code(float x, float inv) {
+  return __float_as_uint(fmaf(x, inv, 6.103515625e-05f) + 12582920.f) & 15u;
+}
+
+}  // namespace eio

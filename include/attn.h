@@ -70,7 +70,7 @@ typedef enum {
   ATTN_ERR_CUDA = 6,            /* a CUDA runtime or driver call failed */
   ATTN_ERR_DEVICE_TIMEOUT = 7,  /* a kernel's bounded wait ran out */
   ATTN_ERR_WORKSPACE = 8,       /* workspace allocation failed */
-  ATTN_ERR_DEVICE_ARG = 9       /* a kernel found a bad device-side argument (seqlens) */
+  ATTN_ERR_DEVICE_ARG = 9       /* a kernel found a bad device-side argument (seqlens, page table) */
 } attn_status;
 
 typedef enum { ATTN_MASK_NONE = 0, ATTN_MASK_CAUSAL = 1, ATTN_MASK_BLOCK = 2 } attn_mask_kind;
@@ -338,6 +338,119 @@ int attn_key_stats(const void* k, float* kbar, float* radius, int B, int Nkv, in
 int attn_fwd_bound(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
                    int Nkv, int d, float scale, int mask_kind, const uint8_t* block_map, const float* kbar,
                    const float* radius, int* n_fallback, void* stream);
+
+/*
+ * ---- Positions, and a KV cache held in 4 bits in pages ----
+ *
+ * The source pages have no counterpart for the calls below; they stand beside
+ * attn_decode for caches too large for 16 bits a value.
+ *
+ * A pool is [n_pages][Hkv][page / 16 tiles] of tiles of 18 d bytes, 16 tokens of
+ * one KV head each: `page` is 16, 32, 64, 128 or 256 tokens, d is 64 or 128.  A
+ * group is 32 channels of one token and head with a bf16 scale s; a code c (4 bits,
+ * 0..15) stands for (c - 8) * s.  With t = 0..3, g = 0..7 and G = d / 32 groups a
+ * tile is, in this order (low nibbles first),
+ *     K codes   [tok][t][group][4 bytes]: channel 32 group + 8 t + n is nibble n
+ *     V codes   [tok / 8][g][tok % 8 / 2][group][tok % 2][2 bytes]: channel
+ *               32 group + 4 g + i is nibble i
+ *     K scales  [tok][group] bf16
+ *     V scales  [tok][group] bf16
+ * table is a device int32 [B][max_pages]: entry j of row b is the page that holds
+ * tokens j * page .. of sequence b; only entries that its length reaches are read.
+ * An entry outside [0, n_pages) that a call reaches latches ATTN_ERR_DEVICE_ARG;
+ * the rows behind it are not written (append), read as zeros (read) or left out
+ * (decode).  seqlens (device int32 [B]) outside [0, max_pages * page] does the same
+ * for the whole sequence.  max_pages * page is at most 2^30.
+ */
+
+/*
+ * attn_rope -- rotary positions with several axes, for q and k in one launch.
+ *
+ * Pair p < n_pairs of every head is rotated by theta = positions[axes[p]] *
+ * freq[p]: (x, y) -> (x cos - y sin, x sin + y cos).  The pair is channels p and
+ * p + d / 2, or 2p and 2p + 1 (interleaved != 0); other channels are copied.
+ * inverse != 0 rotates by -theta, which is also the gradient's map.  theta is
+ * reduced in 64-bit fixed point: its error is below |position| * 2^-63 turns,
+ * whatever the position.
+ *   q, q_out   device, [B, N, Hq, d] (dtype); k, k_out  device, [B, N, Hk, d], Hk may be 0
+ *              q_out may be q (k_out may be k) with the same strides
+ *   positions  device, int32 [B, N, n_axes], the last dimension contiguous
+ *   axes       host, uint8 [n_pairs]; freq  host, fp64 [n_pairs], |freq| <= 65536
+ *   strides    host, int64 [10], in elements: batch and token stride of q, k, q_out,
+ *              k_out and positions.  Heads (stride d) and channels are contiguous.
+ * Limits: d in {32, 64, 128}; dtype ATTN_BF16 or ATTN_F32; 1 <= n_axes <= 4;
+ * strides of q and k multiples of 16 bytes.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA.  Allocates nothing.
+ */
+int attn_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const uint8_t* axes,
+              const double* freq, const int64_t* strides, int B, int N, int Hq, int Hk, int d, int n_axes, int n_pairs,
+              int interleaved, int inverse, int dtype, void* stream);
+
+/*
+ * attn_kv4_append -- K and V rows quantised and written into the cache.
+ *
+ * Per group of 32 channels x: m = max |x|, s = bf16(m / 7) (0 where m < 2^-100;
+ * NaN, with every code 8, where x holds an infinity or a NaN) and
+ * c = 8 + floor(x / s + 1/2), so that |(c - 8) s - x| <= s / 2 up to the rounding of s.
+ *   k, v     device, [B, N, Hkv, d] bf16; heads and channels contiguous
+ *   seqlens  lengths after the append; n_new  device int32 [B] or NULL (N each)
+ *   strides  host, int64 [4], in elements: batch and token stride of k and of v
+ * Row i < n_new[b] becomes token seqlens[b] - n_new[b] + i; later rows (padding) are
+ * not read, and no other byte of the pool changes.  A count outside [0, min(N,
+ * seqlens[b])] latches ATTN_ERR_DEVICE_ARG and appends nothing to that sequence.  No
+ * two appended tokens may share a page slot (a page in two tables is copied first).
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE.
+ */
+int attn_kv4_append(const void* k, const void* v, void* pool, const int32_t* table, const int32_t* seqlens,
+                    const int32_t* n_new, const int64_t* strides, int B, int N, int Hkv, int d, int n_pages, int page,
+                    int max_pages, void* stream);
+
+/*
+ * attn_kv4_read -- rows of the cache as bf16 (for attn_fwd over a cached prefix).
+ *
+ *   k, v   device, [B, N, Hkv, d] bf16 (written): row i of sequence b is token
+ *          start[b] + i, bf16((c - 8) s); zeros at and past seqlens[b]
+ *   start  device int32 [B], or NULL (0); a negative one latches ATTN_ERR_DEVICE_ARG
+ *          and its sequence reads as zeros
+ * Errors: as attn_kv4_append.
+ */
+int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, const int32_t* seqlens,
+                  const int32_t* start, int B, int N, int Hkv, int d, int n_pages, int page, int max_pages,
+                  void* stream);
+
+/*
+ * attn_decode_kv4 -- attn_decode_multi over the 4-bit paged cache.
+ *
+ * The last Sq tokens of each sequence are the queries; token s attends to tokens
+ * 0 .. seqlens[b] - Sq + s.  K and V are (c - 8) s exactly (not rounded to bf16).
+ *   q    device, [B, Sq, Hq, d] bf16; o  device, the same (written)
+ *   lse  device, fp32 [B, Hq, Sq] (written); may be NULL
+ *   workspace  device, attn_decode_kv4_workspace() bytes; its content need not be
+ *              kept or cleared.  Calls that may run at the same time need one each.
+ * Any Hq % Hkv == 0 and any Sq.  A row that sees no token gets O = 0, LSE = -inf.  A query row
+ * that holds an infinity or a NaN gives NaN.  The result does not depend on timing.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE; a bounded wait that
+ * runs out latches ATTN_ERR_DEVICE_TIMEOUT.
+ */
+int attn_decode_kv4(const void* q, const void* pool, const int32_t* table, const int32_t* seqlens, void* o, float* lse,
+                    void* workspace, int64_t workspace_bytes, int B, int Sq, int Hq, int Hkv, int d, int n_pages,
+                    int page, int max_pages, float scale, void* stream);
+
+/* Bytes of workspace that attn_decode_kv4 needs for these sizes (host only; may be 0); -1 for
+ * sizes that it refuses. */
+int64_t attn_decode_kv4_workspace(int B, int Sq, int Hq, int Hkv, int d, int page, int max_pages);
+
+/*
+ * attn_copy_pages -- pages src[i] of a pool copied to pages dst[i], i < n.
+ *
+ *   src, dst  host int32 [n]; read during the call only, so a captured graph keeps its
+ *             own.  A source may repeat; no page may be a destination twice, or a
+ *             source and a destination (ATTN_ERR_SHAPE).
+ *   page_bytes  a multiple of 16; any pool of equal pages will do
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE.  Allocates nothing on the device.
+ */
+int attn_copy_pages(void* pool, int64_t page_bytes, int n_pages, const int32_t* src, const int32_t* dst, int n,
+                    void* stream);
 
 #ifdef __cplusplus
 }
