@@ -9,7 +9,8 @@ append: codes and scales are equal bit for bit.  read: equal bit for bit ((c - 8
 decode: p * s (or p) is rounded to bf16 for the product with V, 2^-8 of each term, and so
   is the output.  A score is a sum of d products and d / 32 scaled parts in fp32 (a tensor core
   may drop, not round: 2^-23 of the running sum a step): off by e = (d + 16) 2^-23 sum|q k|
-  scale, which moves p and its sum by 2 e; ex2 and the sum of p add 2^-20.
+  scale, which moves p and its sum by 2 e; ex2 and the sum of p add 2^-20.  ex2 gives 0
+  below 2^-126 and the largest p is at least 1: each weight may be 2^-126 short as well.
 """
 import math
 
@@ -310,7 +311,9 @@ def _decode_close(o, lse, q, ks, vs, scale):
     ro, rl, w, a = ko.decode(f64(q), ks, vs, scale)
     e = (d + 16) * 2.0 ** -23 * a + 2.0 ** -20
     rel = 2 * e.transpose(0, 2, 1)[..., None]
-    tol = 2.0 ** -8 * (w + np.abs(ro)) * (1 + rel) + rel * w + 2.0 ** -133
+    G = q.shape[2] // ks[0].shape[1]
+    gone = 2.0 ** -126 * np.stack([np.nan_to_num(np.abs(v)).sum(0).repeat(G, 0) for v in vs])[:, None]
+    tol = 2.0 ** -8 * (w + np.abs(ro)) * (1 + rel) + rel * w + gone + 2.0 ** -133
     err = np.abs(f64(o) - ro)
     assert (err <= tol).all(), (float((err - tol).max()), float((err / (tol + 1e-300)).max()))
     if lse is not None:
