@@ -36,6 +36,7 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 int check_pages(int B, int Hkv, int d, int n_pages, int page, int max_pages, Kv4Pages* p) {
   if (B < 1 || Hkv < 1 || n_pages < 1 || max_pages < 1)
     return fail(ATTN_ERR_SHAPE, "B, Hkv, n_pages and max_pages must be >= 1");
+  if (B > (1 << 24) || Hkv > 65535) return fail(ATTN_ERR_SHAPE, "B must be at most 2^24 and Hkv 65535");
   if (d != 64 && d != 128) return fail(ATTN_ERR_UNSUPPORTED, "the 4-bit cache needs d in {64, 128}");
   int shift = 4;
   while (shift <= 8 && page != 1 << shift) ++shift;

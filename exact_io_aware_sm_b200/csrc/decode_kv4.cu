@@ -3,31 +3,32 @@
 //
 //     O = softmax(q K^T scale) V,   K = (ck - 8) sk,  V = (cv - 8) sv
 //
-// The cache is read once: 18 d / 16 bytes a key and KV head, against 1.3
-// instructions a value to widen the codes, so both the memory and the issue
-// slots matter.
+// The cache is read once: 18 d / 16 bytes a key and KV head, against 1.2
+// instructions a value to widen the codes, so the memory, the issue slots and
+// the half-rate integer pipe all matter.
 //
 //   decode_kv4_kernel  persistent, one CTA per SM.  A stage is 32 keys (two
 //     tiles of the cache) of a unit (sequence, KV head, block of at most 8 NCG
 //     columns, a column being a (query head, token) pair of the head's group).
-//     The stages of all units in a row are cut into equal runs, one for each
-//     warp: no counters, and the work of any two warps differs by one stage
-//     whatever the lengths.  Each warp is its own pipeline: a ring of stages
-//     filled by bulk copies (a tile is one contiguous run), an online softmax,
-//     warp-level MMAs on the codes:
-//       S^T (16 keys x 8 columns): per group of 32 channels two MMAs of the
-//         codes c themselves: the bits of a nibble, masked out of the word, are
-//         the fp16 number c 2^-24 or c 2^-20, so widening costs an AND for two
-//         codes.  The -8 is the accumulator's first value (-8 sum q), the group's
-//         scale multiplies the group's sum.  q goes in as fp16, scaled by a power
-//         of two so that its largest magnitude is in [2^14, 2^15): exact down to
-//         2^-28 of that largest.
-//       O^T (d x 8 columns): codes as bf16 (128 + c, less 136), times P sv: the
-//         scale belongs to the key, so it multiplies P before the rounding to bf16
-//         (one rounding for each term, 2^-9, as in attn_decode).
-//     A unit that lies in one warp's run is finished there; the others leave
-//     their numerator, maximum and sum in the workspace.
-//   decode_kv4_combine_kernel  one CTA per query row: joins those.
+//     The stages of all units in a row are cut into equal runs, one for each CTA,
+//     and those into equal runs for its warps: no counters, whatever the lengths.
+//     Each warp is its own pipeline: a ring of stages filled by bulk copies (a
+//     tile is one contiguous run), an online softmax, warp-level MMAs on the
+//     codes.  The bits of a nibble masked out of a word are the fp16 number
+//     c 2^-24, or c 2^-20 four bits higher: widening two codes costs one AND.
+//       S^T (16 keys x 8 columns): two MMAs for each group of 32 channels, whose
+//         scale multiplies their sum; the -8 of c - 8 is the accumulator's first
+//         value (-8 sum q).  q goes in as fp16, scaled by a power of two so that its
+//         largest magnitude is in [2^14, 2^15): exact down to 2^-28 of that.
+//       O^T (d x 8 columns): the scale belongs to the key, so P sv is rounded to
+//         fp16, relative to a power of two (a reference) at least as large as
+//         every scale of the group so far, as P is relative to the running maximum:
+//         2^-12 of each term, and exact to 2^-28 of the largest.  The -8 is taken
+//         off at the end: one more MMA a group keeps 8 sum P sv of the rounded terms.
+//     A unit that lies in one warp's run is finished there, one in a CTA's run by
+//     the CTA once its warps are done; the others leave numerators, maxima and sums.
+//   decode_kv4_combine_kernel  one CTA for each boundary between two runs: joins the
+//     unit that lies across it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,33 +43,49 @@
 namespace eio {
 namespace {
 
-constexpr int kStageKeys = 32;
 constexpr int kMaxCtas = 148;
 constexpr int kRingBudget = 222 * 1024;
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRebase = 8.f;  // move the exponent base only when the maximum grows by more
 
-template <int D, int NCG>
+template <int D, int NCG, int F>
 struct Cfg {
-  static constexpr int W = NCG == 1 ? 12 : 8;  // warps
+#ifndef KV4_W1
+#define KV4_W1 12
+#define KV4_W2 8
+#define KV4_T1 4
+#define KV4_T2 4
+#endif
+  static constexpr int W = NCG == 1 ? KV4_W1 : KV4_W2;  // warps
+  static constexpr int T = NCG == 1 ? KV4_T1 : KV4_T2;  // tiles of a stage
+  static constexpr int kKeys = 16 * T;
   static constexpr int G = D / 32;
+  static constexpr int N = G / F;  // groups, or pairs of groups (F = 2), that share a set of MMA columns
   static constexpr int kTile = kv4_tile_bytes(D);
-  static constexpr int kStage = 2 * kTile;
-  static constexpr int R = kRingBudget / (W * (kStage + 24)) < 8 ? kRingBudget / (W * (kStage + 24)) : 8;
+  static constexpr int kStage = T * kTile;
+  static constexpr int kFit = kRingBudget / (W * (kStage + 24));
+  static constexpr int R = kFit < 8 ? kFit : 8;  // stages of a warp's ring
   static constexpr int kOffMeta = W * R * kStage;
   static constexpr int kOffBars = kOffMeta + W * R * 16;
-  static constexpr int kSmem = kOffBars + W * R * 8 + 128;
-  static constexpr int kCols = 8 * NCG;
+  static constexpr int kOffSegs = kOffBars + W * R * 8;
+  static constexpr int kSmem = kOffSegs + 2 * W * 16;
+  static constexpr int kCols = 8 * NCG / F;
   static constexpr int kSlotFloats = kCols * (D + 2);  // numerators [col][D], then (maximum, sum) [col]
+  static constexpr int kSlots = 2 * W + 2;             // of a CTA: two a warp, two for what leaves the CTA
 };
 
-// How a call's stages are laid out and cut, the same for both kernels.
-struct Split {
-  long long total;  // stages
-  long long parts;  // runs: part i is stages [i total / parts, (i + 1) total / parts)
-  __device__ long long first(long long i) const { return i * total / parts; }
-  __device__ long long part_of(long long x) const { return ((x + 1) * parts - 1) / total; }
+// Where the run of a CTA starts: stage x of all, stage st (of nst) of unit u of sequence b.
+struct Run {
+  long long x;
+  int b, u, st, nst;
+  long long pad;
+};
+
+// A segment (the part of a unit in a warp's run) that is not a whole unit.
+struct Segment {
+  int b, u;   // b < 0: none
+  int starts, ends;
 };
 
 __device__ __forceinline__ int checked_len(const Kv4Pages& p, int b) {
@@ -80,20 +97,21 @@ __device__ __forceinline__ int checked_len(const Kv4Pages& p, int b) {
   return len;
 }
 
-// D (16x8 f32) = A (16x16 f16, row) * B (16x8 f16, col) + C.
-__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+// D (16x8 f32) += A (16x16, row) * B (16x8, col), f16 and bf16; free to be scheduled.
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// Nibble 4 i of both halves of w as bf16 numbers c - 8.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  uint32_t x = (w & 0x000f000fu) | 0x43004300u;  // 128 + c
-  __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), __floats2bfloat162_rn(136.f, 136.f));
-  return *reinterpret_cast<uint32_t*>(&v);
+__device__ __forceinline__ void mma_f16_first(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_first(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 template <int G>
@@ -107,32 +125,40 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-// G bf16 scales as fp32.
+// G bf16 scales, packed.
 template <int G>
-__device__ __forceinline__ void lds_scales(const uint8_t* p, float* s) {
-  uint32_t w[G / 2];
+__device__ __forceinline__ void lds_scales(const uint8_t* p, uint32_t* w) {
   if constexpr (G == 4) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
     w[0] = u.x, w[1] = u.y;
   } else {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
-#pragma unroll
-  for (int i = 0; i < G / 2; ++i) {
-    s[2 * i] = __uint_as_float(w[i] << 16);
-    s[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
 }
+
+// An 8 x 8 tile of 16-bit values transposed (free to be scheduled, unlike movmatrix_trans).
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 struct Columns {
   int blocks, per;  // column blocks of a KV head's group, columns of each (the last may have fewer)
 };
 
-template <int D, int NCG>
-__global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
-    decode_kv4_kernel(const DecodeKv4Args a, const Columns cols, long long* start, float* slots) {
-  using C = Cfg<D, NCG>;
-  constexpr int R = C::R, G = C::G;
+template <int D, int NCG, int F>
+__global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
+    decode_kv4_kernel(const DecodeKv4Args a, const Columns cols, Run* runs, float* slots) {
+  using C = Cfg<D, NCG, F>;
+  constexpr int R = C::R, G = C::G, W = C::W;
   extern __shared__ __align__(128) uint8_t smem[];
   const Kv4Pages& pg = a.pages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -140,42 +166,45 @@ __global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
   uint8_t* ring = smem + warp * R * C::kStage;
   int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * R;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBars) + warp * R;
+  Segment* segs = reinterpret_cast<Segment*>(smem + C::kOffSegs);
   const int units = pg.Hkv * cols.blocks;
   const int heads = a.Hq / pg.Hkv, live_cols = heads * a.Sq;
+  const int tiles_shift = pg.page_shift - 4;
+  float* const my_slots = slots + static_cast<size_t>(blockIdx.x) * C::kSlots * C::kSlotFloats;
 
   if (lane == 0) {
     for (int r = 0; r < R; ++r) mbar_init(&bars[r], 1);
     fence_mbar_init();
   }
+  if (lane < 2) segs[2 * warp + lane].b = -1;
   pdl_launch_dependents();
   __syncwarp();
 
-  // All stages of the call; the first CTA's first warp leaves where each sequence starts for the second kernel.
-  Split sp;
-  {
-    long long sum = 0;
-    for (int b = lane; b < pg.B; b += 32) sum += (checked_len(pg, b) + kStageKeys - 1) / kStageKeys;
+  // The stages of the call, cut for the CTAs and then for the warps of each.
+  const int len0 = lane < pg.B ? checked_len(pg, lane) : 0;  // of the first 32 sequences
+  long long total = (len0 + C::kKeys - 1) / C::kKeys;
+  for (int b = lane + 32; b < pg.B; b += 32) total += (checked_len(pg, b) + C::kKeys - 1) / C::kKeys;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    sp.total = sum * units;
-    const long long warps = static_cast<long long>(gridDim.x) * C::W;
-    sp.parts = sp.total < warps ? sp.total : warps;
-  }
-  const bool scribe = blockIdx.x == 0 && warp == 0;
-  // Parts go round the CTAs, so that few of them still use every SM.
-  const long long part = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
-  const bool idle = part >= sp.parts;
-  if (idle && !scribe) return;
-  const long long x0 = idle ? 0 : sp.first(part), x1 = idle ? 0 : sp.first(part + 1);
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  total *= units;
+  const unsigned ctas = gridDim.x, cta = blockIdx.x;
+  const long long each = total >> 32 ? total / ctas : static_cast<unsigned>(total) / ctas;
+  const unsigned more = static_cast<unsigned>(total - each * ctas);
+  const long long cta_x = each * cta + min(cta, more);
+  const long long n_cta = each + (cta < more);
+  const long long each_w = n_cta >> 32 ? n_cta / W : static_cast<unsigned>(n_cta) / W;
+  const unsigned more_w = static_cast<unsigned>(n_cta - each_w * W);
+  const long long x0 = cta_x + each_w * warp + min(static_cast<unsigned>(warp), more_w);
+  int left = static_cast<int>(each_w + (warp < more_w));  // stages still to be produced
+  const int mine = left;
 
-  // The producer's place: stage st (of nst) of unit u of sequence b.
-  int b = 0, u = 0, st = 0, nst = 0, len = 0;
-  {
+  // The producer's place: stage st (of nst) of column block cb of KV head h of sequence b.
+  int b = 0, h = 0, cb = 0, st = 0, nst = 0, len = 0;
+  if (mine > 0) {
     long long base = 0;  // stages of a KV head before this group of 32 sequences
-    bool found = idle;
-    for (int c = 0; c < pg.B && (scribe || !found); c += 32) {
-      const int l = c + lane < pg.B ? checked_len(pg, c + lane) : 0;
-      const int n = (l + kStageKeys - 1) / kStageKeys;
+    for (int c = 0; c < pg.B; c += 32) {
+      const int l = c == 0 ? len0 : c + lane < pg.B ? checked_len(pg, c + lane) : 0;
+      const int n = (l + C::kKeys - 1) / C::kKeys;
       long long pre = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -183,34 +212,50 @@ __global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
         if (lane >= off) pre += v;
       }
       pre += base;
-      if (scribe && c + lane < pg.B) start[1 + c + lane] = pre;
       const unsigned past = __ballot_sync(0xffffffffu, pre * units > x0);
-      if (!found && past) {
+      if (past) {
         const int src = __ffs(past) - 1;
         b = c + src;
         len = __shfl_sync(0xffffffffu, l, src);
         nst = __shfl_sync(0xffffffffu, n, src);
-        const long long before = __shfl_sync(0xffffffffu, pre, src) - nst;
-        const long long in = x0 - before * units;
-        u = static_cast<int>(in / nst);
-        st = static_cast<int>(in % nst);
-        found = true;
+        const long long in = x0 - (__shfl_sync(0xffffffffu, pre, src) - nst) * units;
+        const int u = static_cast<int>(in >> 32 ? in / nst : static_cast<unsigned>(in) / static_cast<unsigned>(nst));
+        st = static_cast<int>(in - static_cast<long long>(u) * nst);
+        h = u / cols.blocks;
+        cb = u - h * cols.blocks;
+        break;
       }
       base = __shfl_sync(0xffffffffu, pre, 31);
     }
-    if (scribe && lane == 0) start[0] = 0;
   }
-  if (idle) return;
+  if (warp == 0 && lane == 0) {
+    runs[cta] = Run{cta_x, b, h * cols.blocks + cb, st, nst, 0};
+    if (cta + 1 == ctas) runs[ctas].x = total;
+  }
+  if (warp == W - 1) {  // sequences without a token are shared out among the CTAs
+    for (int b0 = cta; b0 < pg.B; b0 += 32 * ctas) {
+      const int bl = b0 + lane * ctas;
+      unsigned none = __ballot_sync(0xffffffffu, bl < pg.B && checked_len(pg, bl) == 0);
+      for (; none; none &= none - 1) {
+        const size_t be = b0 + (__ffs(none) - 1) * ctas;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + be * a.Sq * a.Hq * D);
+        for (int i = lane; i < a.Sq * a.Hq * (D / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse)
+          for (int i = lane; i < a.Sq * a.Hq; i += 32) a.lse[be * a.Sq * a.Hq + i] = -INFINITY;
+      }
+    }
+  }
 
-  int left = static_cast<int>(x1 - x0);  // stages still to be produced
-  bool fresh = true;                     // the next one is its run's first of a unit
-  int win = 0, ids = 0;                  // lane i holds the page id of page win + i of sequence b
-  bool no_win = true;
-  const int tiles_shift = pg.page_shift - 4;
+  bool fresh = true;           // the next stage is its run's first of a unit
+  int win = 0, ids = 0;        // lane i holds the page id of page win + i of sequence b
+  int win_end = 0;             // 0: no such window yet
+  int in_page = 0;             // stages left in the page at src
+  const uint8_t* src = nullptr;
+  const long long page_bytes = static_cast<long long>(pg.Hkv << tiles_shift) * C::kTile;
   auto page_of = [&](int p) -> int {
-    if (no_win || p - win >= 32 || p < win) {
+    if (p >= win_end) {
       win = p;
-      no_win = false;
+      win_end = p + 32;
       ids = 0;
       if ((static_cast<long long>(p + lane) << pg.page_shift) < len) {
         ids = pg.table[static_cast<size_t>(b) * pg.max_pages + p + lane];
@@ -222,70 +267,123 @@ __global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
     }
     return __shfl_sync(0xffffffffu, ids, p - win);
   };
+  int missing = 0;  // the page at src does not exist
   auto produce = [&](int slot) {
     if (st == nst) {  // the next unit, in the next sequence that has one
       st = 0;
       fresh = true;
-      no_win = true;
-      if (++u == units) {
-        u = 0;
-        do {
-          ++b;
-          len = checked_len(pg, b);
-        } while (len == 0 && b + 1 < pg.B);
-        nst = (len + kStageKeys - 1) / kStageKeys;
+      win_end = 0;
+      in_page = 0;
+      if (++cb == cols.blocks) {
+        cb = 0;
+        if (++h == pg.Hkv) {
+          h = 0;
+          do {
+            ++b;
+            len = b < pg.B ? checked_len(pg, b) : 1;  // past the end only where lengths changed under the call
+          } while (len == 0);
+          b = min(b, pg.B - 1);
+          nst = (len + C::kKeys - 1) / C::kKeys;
+        }
       }
     }
-    const int k0 = st * kStageKeys;
-    const int ntiles = len - k0 > 16 ? 2 : 1;
-    const int p0 = page_of(k0 >> pg.page_shift);
-    const int h = u / cols.blocks;
-    const uint8_t* src = pg.pool + (((static_cast<long long>(p0) * pg.Hkv + h) << tiles_shift) + ((k0 >> 4) & ((1 << tiles_shift) - 1))) * C::kTile;
+    const int k0 = st * C::kKeys;
+    const int ntiles = min((len - k0 + 15) >> 4, C::T);
     uint8_t* dst = ring + slot * C::kStage;
-    int bad = p0 < 0 ? 3 : 0;
-    uint32_t bytes = p0 < 0 ? 0 : ntiles * C::kTile;
-    const uint8_t* src1 = nullptr;
-    if (tiles_shift == 0) {  // pages of one tile: the second tile is elsewhere
-      if (bytes) bytes = C::kTile;
-      bad &= 1;
-      if (ntiles == 2) {
-        const int p1 = page_of((k0 >> 4) + 1);
-        if (p1 < 0) bad |= 2;
-        else src1 = pg.pool + (static_cast<long long>(p1) * pg.Hkv + h) * C::kTile;
+    uint64_t* bar = &bars[slot];
+    int bad = 0;
+    if (1 << tiles_shift >= C::T) {
+      if (in_page == 0) {
+        const int p = page_of(k0 >> pg.page_shift);
+        const int at = (k0 >> 4) & ((1 << tiles_shift) - 1);
+        missing = p < 0 ? (1 << C::T) - 1 : 0;
+        src = pg.pool + max(p, 0) * page_bytes + ((static_cast<long long>(h) << tiles_shift) + at) * C::kTile;
+        in_page = ((1 << tiles_shift) - at) / C::T;
       }
+      bad = missing;
+      const uint32_t bytes = bad ? 0 : ntiles * C::kTile;
+      mbar_arrive_expect_tx_elect(bar, bytes);
+      if (bytes) bulk_load_elect(dst, src, bytes, bar);
+      src += C::kStage;
+      --in_page;
+    } else {  // a stage of several pages
+      const uint8_t* at[C::T];
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int i = 0; i < C::T; ++i) {
+        at[i] = nullptr;
+        if (i < ntiles && (i & ((1 << tiles_shift) - 1)) == 0) {
+          const int p = page_of((k0 >> pg.page_shift) + (i >> tiles_shift)), nt = min(1 << tiles_shift, ntiles - i);
+          if (p < 0) {
+            bad |= ((1 << nt) - 1) << i;
+          } else {
+            at[i] = pg.pool + p * page_bytes + (static_cast<long long>(h) << tiles_shift) * C::kTile;
+            bytes += nt * C::kTile;
+          }
+        }
+      }
+      mbar_arrive_expect_tx_elect(bar, bytes);
+#pragma unroll
+      for (int i = 0; i < C::T; ++i)
+        if (at[i]) bulk_load_elect(dst + i * C::kTile, at[i], min(1 << tiles_shift, ntiles - i) * C::kTile, bar);
     }
     --left;
-    const int flags = (fresh ? 1 : 0) | (st + 1 == nst || left == 0 ? 2 : 0) | bad << 2;
-    fresh = false;
-    if (lane == 0) meta[slot] = make_int4(b, u, k0 | flags, len);
-    fence_proxy_async_smem();  // earlier generic accesses to this slot come first
-    mbar_arrive_expect_tx_elect(&bars[slot], bytes + (src1 ? C::kTile : 0));
-    if (bytes) bulk_load_elect(dst, src, bytes, &bars[slot]);
-    if (src1) bulk_load_elect(dst + C::kTile, src1, C::kTile, &bars[slot]);
     ++st;
+    const int flags = (fresh ? 1 : 0) | (st == nst || left == 0 ? 2 : 0) | bad << 2;
+    fresh = false;
+    if (lane == 0) meta[slot] = make_int4(b, h * cols.blocks + cb, k0 | flags, len);
   };
 
-  uint32_t produced = 0, consumed = 0;
-  for (int r = 0; r < R && left > 0; ++r, ++produced) produce(r);
+  const int b0_ = b, u0_ = h * cols.blocks + cb, len0_ = len;
+  int produced = 0, consumed = 0;
+  for (; produced < R && left > 0; ++produced) produce(produced);
   __syncwarp();
 
-  uint32_t qf[NCG][G][4];       // B fragments of q: two MMAs a group
-  float bias[NCG][G][2];        // -8 sum of q over a group, columns 2t and 2t + 1
-  float fac[NCG][2];            // a raw score times this is the score in log2 units
-  int vis[NCG][2];              // keys that the column sees
-  float acc[NCG][G][2][4];      // O^T: channels 32 group + 4 g + 2 j (and + 1), columns 2t, 2t + 1
+  // Columns.  An MMA has 8; with F = 2 the upper four repeat the lower four for the odd groups (of a pair
+  // of groups), so that one accumulator holds both groups' sums and a lane scales only its own group's.  This lane:
+  // column g as a row of q (and of the B operands), columns 2 t and 2 t + 1 of the accumulators.
+  constexpr int NS = C::N;
+  const int half_q = F == 2 ? g >> 2 : 0, half = F == 2 ? t >> 1 : 0;
+  const uint32_t pick = half ? 0x3244u : 0x1044u;  // F = 2: this lane's scale of a packed pair, as fp32
+  int at_cb = -1;                 // the column block they are for
+  int q_at[NCG], o_at[NCG][2];    // (token Hq + head in the group); -1: no such column
+  int tok[NCG][2];                // the column's token
+  uint32_t qf[NCG][G][4];         // B fragments of q: two MMAs a group
+  uint32_t less[NCG][2];          // B fragment of -8 sum of q over each group, in four bf16 parts
+  float fac[NCG][2];              // a raw score times this is the score in log2 units
+  int vis[NCG][2];                // keys that the column sees
+  float acc[NCG][G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and + 1: 16 times as large), columns 2 t, 2 t + 1
+  float psum[NCG][NS][4];         // 8 sum of P sv, as rounded: columns 2 t and 2 t + 1, twice
   float m[NCG][2], l[NCG][2];
+  float rinv[NS];                 // P sv goes in times this: 2^6 over the reference of the lane's group
+  uint32_t ref[G / 2];            // the references as bf16, packed like the scales
   int seg_k0 = 0, which = 0;
   bool ok = true;
 
   auto begin_unit = [&](int ub, int uu, int ulen) {
-    const int h = uu / cols.blocks, c0 = uu % cols.blocks * cols.per;
+    const int uh = cols.blocks == 1 ? uu : uu / cols.blocks, ucb = uu - uh * cols.blocks;
+    if (ucb != at_cb) {
+      at_cb = ucb;
+#pragma unroll
+      for (int cg = 0; cg < NCG; ++cg)
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int c = (cg * 8 + (j < 2 ? 2 * t + j : g)) & (C::kCols - 1), col = ucb * cols.per + c;
+          const int hd = col / a.Sq, tk = col - hd * a.Sq;
+          const int at = c < cols.per && col < live_cols ? tk * a.Hq + hd : -1;
+          if (j < 2) {
+            o_at[cg][j] = at;
+            tok[cg][j] = tk;
+          } else {
+            q_at[cg] = at;
+          }
+        }
+    }
+    const size_t row0 = static_cast<size_t>(ub) * a.Sq * a.Hq + uh * heads;
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg) {
-      const int c = cg * 8 + g, col = c0 + c;
-      const bool live = c < cols.per && col < live_cols;
-      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) +
-                                 ((static_cast<size_t>(ub) * a.Sq + (live ? col % a.Sq : 0)) * a.Hq + h * heads + (live ? col / a.Sq : 0)) * D + 8 * t;
+      const bool live = q_at[cg] >= 0;
+      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) + (row0 + (live ? q_at[cg] : 0)) * D + 8 * t;
       uint4 raw[G];
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) raw[grp] = live ? *reinterpret_cast<const uint4*>(row + 32 * grp) : make_uint4(0u, 0u, 0u, 0u);
@@ -294,13 +392,14 @@ __global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
       for (int grp = 0; grp < G; ++grp) {
         const uint32_t w[4] = {raw[grp].x, raw[grp].y, raw[grp].z, raw[grp].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx = max(mx, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
       }
+      mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int e = min(max(141 - static_cast<int>(mx >> 7), -100), 100);  // q 2^e
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      float fc = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - e) << 23);
+      const float up = pow2(e), fc = a.scale_log2 * pow2(24 - e);
+      float sums[G];
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) {
         const uint32_t w[4] = {raw[grp].x, raw[grp].y, raw[grp].z, raw[grp].w};
@@ -315,76 +414,181 @@ __global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
         for (int n = 0; n < 4; ++n) {
           const float f = n & 1 ? 1.f / 16.f : 1.f;
           const __half2 v = __floats2half2_rn(x[n] * f, x[n + 4] * f);
-          qf[cg][grp][n] = *reinterpret_cast<const uint32_t*>(&v);
+          qf[cg][grp][n] = F == 1 || half_q == (grp & 1) ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
           const float2 back = __half22float2(v);
           sum += (back.x + back.y) * (n & 1 ? 16.f : 1.f);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -8.f * 5.9604644775390625e-08f;  // 2^-24
+        sums[grp] = sum * (-8.f * pow2(-24));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) bias[cg][grp][j] = __shfl_sync(0xffffffffu, sum, (2 * t + j) * 4);
+        for (int i = 0; i < 4; ++i) acc[cg][grp][0][i] = acc[cg][grp][1][i] = psum[cg][grp / F][i] = 0.f;
+      }
+      // Row k of this operand is part k / G of group k % G (d = 128: parts 0 and 1 in b0, 2 and 3 in b1;
+      // d = 64: 0 to 3 in b0), so that a row of K's scales, repeated, is the other operand.
+      float x0 = sums[0], x1 = sums[1];
+      if constexpr (G == 4) {
+        if (t & 1) x0 = sums[2], x1 = sums[3];
+      }
+      uint32_t parts[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[cg][grp][j][i] = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+        parts[i] = half_q ? 0u : *reinterpret_cast<const uint32_t*>(&h);
+        x0 -= __uint_as_float(parts[i] << 16);
+        x1 -= __uint_as_float(parts[i] & 0xffff0000u);
+      }
+      if constexpr (G == 4) {
+        less[cg][0] = t < 2 ? parts[0] : parts[1];
+        less[cg][1] = t < 2 ? parts[2] : parts[3];
+      } else {
+        less[cg][0] = t == 0 ? parts[0] : t == 1 ? parts[1] : t == 2 ? parts[2] : parts[3];
+        less[cg][1] = 0;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         fac[cg][j] = __shfl_sync(0xffffffffu, fc, (2 * t + j) * 4);
-        vis[cg][j] = ulen - a.Sq + 1 + (c0 + cg * 8 + 2 * t + j) % a.Sq;
+        vis[cg][j] = ulen - a.Sq + 1 + tok[cg][j];
         m[cg][j] = -INFINITY;
         l[cg][j] = 0.f;
       }
     }
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) ref[i] = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) rinv[i] = pow2(106);
   };
 
-  // One stage: keys k0 .. k0 + 31.  EDGE: some key is past a column's last one, or its page is missing.
-  auto stage = [&](auto edge_c, const uint8_t* base, int k0, int bad, int ntiles) {
-    constexpr bool EDGE = decltype(edge_c)::value;
-    float s[2][NCG][4];
-    auto masked = [&](int tile, int cg, int i) {
-      return (bad >> tile & 1) || k0 + tile * 16 + g + (i >> 1) * 8 >= vis[cg][i & 1];
-    };
+  // This lane's scale of set n (its group, or the lane's one of its pair) among packed scales.
+  auto scale_at = [&](const uint32_t* w, int n) -> float {
+    if constexpr (F == 2) return __uint_as_float(__byte_perm(w[n], 0u, pick));
+    else return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
+  };
+
+  // References that hold the V scales of two tiles (rows of this lane; infinities and NaNs keep theirs):
+  // 4 times the largest, so that they seldom move.
+  auto move_refs = [&](const uint32_t (*vs)[2][G / 2]) {
 #pragma unroll
-    for (int tile = 0; tile < 2; ++tile) {
-      if (EDGE && tile >= ntiles) {
+    for (int grp = 0; grp < G; ++grp) {
+      uint32_t x = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = vs[i >> 1][i & 1][grp >> 1] >> (16 * (grp & 1)) & 0x7fffu;
+        x = max(x, v < 0x7f80u ? v : 0u);
+      }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
+      const uint32_t old = ref[grp >> 1] >> (16 * (grp & 1)) & 0xffffu;
+      if (x > old) {
+        const int e = min(max(static_cast<int>(x >> 7) + 3, 27), 254);  // biased exponent of the new reference
+        const float down = old == 0 ? 0.f : pow2(max(static_cast<int>(old >> 7) - e, -126));
+        const bool own = F == 1 || half == (grp & 1);
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[tile][cg][i] = -INFINITY;
-        continue;
+          for (int i = 0; i < 4; ++i) {
+            if (own) psum[cg][grp / F][i] *= down;
+            acc[cg][grp][0][i] *= down;
+            acc[cg][grp][1][i] *= down;
+          }
+        if (own) rinv[grp / F] = pow2(max(6 + 127 - e, -126));
+        const uint32_t bits = static_cast<uint32_t>(e) << 7;
+        ref[grp >> 1] = grp & 1 ? (ref[grp >> 1] & 0xffffu) | bits << 16 : (ref[grp >> 1] & 0xffff0000u) | bits;
       }
+    }
+  };
+
+  // Two tiles of a stage: keys k0 .. k0 + 31; bit i of bad: the page of tile i is missing.
+  auto two_tiles = [&](const uint8_t* base, int k0, int bad, int ulen) {
+    float s[2][NCG][4];
+    uint32_t vs[2][2][G / 2], top[G / 2] = {};
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
       const uint8_t* p = base + tile * C::kTile;
-      uint32_t w[2][G];
-      float ks[2][G];
+      uint32_t w[2][G], ks[2][G / 2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         lds_words<G>(p + ((g + 8 * r) * 4 + t) * (4 * G), w[r]);
         lds_scales<G>(p + kv4_off_ks(D) + (g + 8 * r) * (2 * G), ks[r]);
+        lds_scales<G>(p + kv4_off_vs(D) + (g + 8 * r) * (2 * G), vs[tile][r]);
       }
+      const uint32_t lo = *reinterpret_cast<const uint32_t*>(p + kv4_off_ks(D) + g * (2 * G) + (t % (G / 2)) * 4);
+      const uint32_t hi = *reinterpret_cast<const uint32_t*>(p + kv4_off_ks(D) + (g + 8) * (2 * G) + (t % (G / 2)) * 4);
+      const uint32_t sc[4] = {lo, hi, lo, hi};
+#pragma unroll
+      for (int cg = 0; cg < NCG; ++cg) mma_bf16_first(s[tile][cg], sc, less[cg][0], less[cg][1]);
+      float raw[NCG][4];
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) {
         const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[1][grp] & 0x000f000fu, w[0][grp] & 0x00f000f0u, w[1][grp] & 0x00f000f0u};
         const uint32_t v0 = w[0][grp] >> 8, v1 = w[1][grp] >> 8;
         const uint32_t f1[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u};
+        const float k_lo = scale_at(ks[0], grp / F), k_hi = scale_at(ks[1], grp / F);
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg) {
-          float raw[4];
-          mma_f16(raw, f0, qf[cg][grp][0], qf[cg][grp][1], bias[cg][grp][0], bias[cg][grp][1], bias[cg][grp][0], bias[cg][grp][1]);
-          mma_f16(raw, f1, qf[cg][grp][2], qf[cg][grp][3], raw[0], raw[1], raw[2], raw[3]);
+          if (grp % F == 0) mma_f16_first(raw[cg], f0, qf[cg][grp][0], qf[cg][grp][1]);
+          else mma_f16(raw[cg], f0, qf[cg][grp][0], qf[cg][grp][1]);
+          mma_f16(raw[cg], f1, qf[cg][grp][2], qf[cg][grp][3]);
+          if (grp % F == F - 1) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[tile][cg][i] = grp == 0 ? raw[i] * ks[i >> 1][0] : fmaf(raw[i], ks[i >> 1][grp], s[tile][cg][i]);
+            for (int i = 0; i < 4; ++i) s[tile][cg][i] = fmaf(raw[cg][i], i < 2 ? k_lo : k_hi, s[tile][cg][i]);
+          }
         }
       }
-      if constexpr (EDGE) {
+      if constexpr (F == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[tile][0][i] += __shfl_xor_sync(0xffffffffu, s[tile][0][i], 2);
+      }
+    }
+    if (bad || k0 + 32 > ulen - a.Sq + 1) {  // some key is past a column's last one, or its page is missing
+      uint32_t odd = 0;                       // V scales that are not finite, of keys that are there
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int key = k0 + tile * 16 + 8 * r + g;
+          const bool gone = (bad >> tile & 1) || key >= ulen;
+#pragma unroll
+          for (int cg = 0; cg < NCG; ++cg)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (gone || key >= vis[cg][j]) s[tile][cg][2 * r + j] = -INFINITY;
+          // what is not there has no weight and moves no reference; a key that is there, but not for
+          // every column, must not bring its NaN to the others (0 NaN = NaN): out here, in below
+#pragma unroll
+          for (int i = 0; i < G / 2; ++i) {
+            uint32_t& v = vs[tile][r][i];
+            if (gone) v = 0;
+            if ((v & 0x7f80u) == 0x7f80u) odd |= 1u << (tile * 16 + r * 8 + 2 * i), v &= 0xffff0000u;
+            if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (tile * 16 + r * 8 + 2 * i), v &= 0xffffu;
+          }
+        }
+      if (__any_sync(0xffffffffu, odd != 0)) {
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (masked(tile, cg, i)) s[tile][cg][i] = -INFINITY;
+          for (int j = 0; j < 2; ++j) {
+            uint32_t sees = 0;  // groups in which this column sees one
+            for (int tr = 0; tr < 4; ++tr)
+              if (k0 + tr * 8 + g < vis[cg][j]) sees |= odd >> (tr * 8);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) sees |= __shfl_xor_sync(0xffffffffu, sees, off);
+#pragma unroll
+            for (int grp = 0; grp < G; ++grp)
+              if (sees >> grp & 1) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[cg][grp][i][j] = acc[cg][grp][i][j + 2] = __uint_as_float(0x7fffffffu);
+              }
+          }
       }
     }
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) top[i] = __vmaxu2(__vmaxu2(vs[0][0][i], vs[0][1][i]), __vmaxu2(vs[1][0][i], vs[1][1][i]));
+    bool over = false;
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) over |= __vmaxu2(top[i], ref[i]) != ref[i];
+    if (__any_sync(0xffffffffu, over)) move_refs(vs);
+    float mneg[NCG][2];
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
@@ -404,57 +608,57 @@ __global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
               acc[cg][grp][i][j] *= alpha;
               acc[cg][grp][i][j + 2] *= alpha;
             }
+#pragma unroll
+          for (int n = 0; n < NS; ++n) psum[cg][n][j] *= alpha;
           m[cg][j] = v;
         }
+        mneg[cg][j] = m[cg][j] == -INFINITY ? 0.f : -m[cg][j];  // a column that has seen no key yet: its p are 0
       }
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
-      if (EDGE && tile >= ntiles) continue;
       const uint8_t* p = base + tile * C::kTile;
+      uint32_t w[2][G];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) lds_words<G>(p + kv4_off_v(D) + ((r * 8 + g) * 4 + t) * (4 * G), w[r]);
 #pragma unroll
       for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float mb = m[cg][i & 1];  // -inf in a column that has seen no key yet: its p are 0
           float& x = s[tile][cg][i];
-          x = wm_ex2(fmaf(x, fac[cg][i & 1], EDGE && mb == -INFINITY ? 0.f : -mb));
+          x = wm_ex2(fmaf(x, fac[cg][i & 1], mneg[cg][i & 1]));
           l[cg][i & 1] += x;
         }
-      uint32_t w[2][G];
-      float vs[2][G];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        lds_words<G>(p + kv4_off_v(D) + ((r * 8 + g) * 4 + t) * (4 * G), w[r]);
-        lds_scales<G>(p + kv4_off_vs(D) + (g + 8 * r) * (2 * G), vs[r]);
-      }
-#pragma unroll
-      for (int grp = 0; grp < G; ++grp) {
-        uint32_t pb[NCG][2];
+      for (int n = 0; n < NS; ++n) {
+        const float v_lo = scale_at(vs[tile][0], n) * rinv[n], v_hi = scale_at(vs[tile][1], n) * rinv[n];
+        const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+        uint32_t b0[NCG], b1[NCG];
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg) {
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = s[tile][cg][i] * vs[i >> 1][grp];
-            if (EDGE && masked(tile, cg, i)) x[i] = 0.f;  // whatever the scale of a masked key holds
-          }
-          pb[cg][0] = movmatrix_trans(wm_pack_bf16x2(x[0], x[1]));
-          pb[cg][1] = movmatrix_trans(wm_pack_bf16x2(x[2], x[3]));
+          b0[cg] = transposed(pack_f16x2(s[tile][cg][0] * v_lo, s[tile][cg][1] * v_lo));
+          b1[cg] = transposed(pack_f16x2(s[tile][cg][2] * v_hi, s[tile][cg][3] * v_hi));
+          mma_f16(psum[cg][n], eights, b0[cg], b1[cg]);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t af[4] = {code_pair(w[0][grp] >> (8 * j)), code_pair(w[0][grp] >> (8 * j + 4)),
-                                  code_pair(w[1][grp] >> (8 * j)), code_pair(w[1][grp] >> (8 * j + 4))};
+        for (int grp = n * F; grp < n * F + F; ++grp) {
+          const uint32_t v0 = w[0][grp] >> 8, v1 = w[1][grp] >> 8;
+          const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[0][grp] & 0x00f000f0u, w[1][grp] & 0x000f000fu, w[1][grp] & 0x00f000f0u};
+          const uint32_t f1[4] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu, v1 & 0x00f000f0u};
 #pragma unroll
-          for (int cg = 0; cg < NCG; ++cg) mma_16816(acc[cg][grp][j], af, pb[cg][0], pb[cg][1]);
+          for (int cg = 0; cg < NCG; ++cg) {
+            mma_f16(acc[cg][grp][0], f0, b0[cg], b1[cg]);
+            mma_f16(acc[cg][grp][1], f1, b0[cg], b1[cg]);
+          }
         }
       }
     }
   };
 
-  auto end_unit = [&](int ub, int uu, bool whole) {
-    const int h = uu / cols.blocks, c0 = uu % cols.blocks * cols.per;
-    float* slot = slots + (2 * part + which) * C::kSlotFloats;
+  auto end_unit = [&](int ub, int uu, bool starts, bool ends) {
+    const int uh = cols.blocks == 1 ? uu : uu / cols.blocks;
+    const size_t row0 = static_cast<size_t>(ub) * a.Sq * a.Hq + uh * heads;
+    float* slot = my_slots + (2 * warp + which) * C::kSlotFloats;
+    const bool whole = starts && ends;
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
@@ -463,135 +667,199 @@ __global__ void __launch_bounds__(Cfg<D, NCG>::W * 32, 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int c = cg * 8 + 2 * t + j, col = c0 + c;
-        if (c < cols.per && col < live_cols) {
-          if (whole) {
-            const int hq = h * heads + col / a.Sq, sq = col % a.Sq;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((static_cast<size_t>(ub) * a.Sq + sq) * a.Hq + hq) * D + 4 * g;
+        if (o_at[cg][j] >= 0) {
+          const int c = (cg * 8 + 2 * t + j) & (C::kCols - 1);
+          const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (row0 + o_at[cg][j]) * D + 4 * g + 32 * half;
+          float* part = slot + c * D + 4 * g + 32 * half;
 #pragma unroll
-            for (int grp = 0; grp < G; ++grp) {
-              const float* x = acc[cg][grp][0];
-              const float* y = acc[cg][grp][1];
-              *reinterpret_cast<uint2*>(o + 32 * grp) =
-                  make_uint2(wm_pack_bf16x2(x[j] * inv, x[j + 2] * inv), wm_pack_bf16x2(y[j] * inv, y[j + 2] * inv));
-            }
-            if (g == 0 && a.lse) a.lse[(static_cast<size_t>(ub) * a.Hq + hq) * a.Sq + sq] = sum == 0.f ? -INFINITY : (m[cg][j] + log2f(sum)) * kLn2;
-          } else {
-            float* o = slot + c * D + 4 * g;
+          for (int n = 0; n < NS; ++n) {
+            // 1 / rinv, exactly; raw numerators are in units of 2^-24 (2^-20: odd channels)
+            const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv, less8 = psum[cg][n][j] * pow2(24);
+            float y[4];
 #pragma unroll
-            for (int grp = 0; grp < G; ++grp) {
-              const float* x = acc[cg][grp][0];
-              const float* y = acc[cg][grp][1];
-              *reinterpret_cast<float4*>(o + 32 * grp) = make_float4(x[j], x[j + 2], y[j], y[j + 2]);
+            for (int i = 0; i < 4; ++i) {
+              const float own = half ? acc[cg][F * n + F - 1][i >> 1][j + 2 * (i & 1)] : acc[cg][F * n][i >> 1][j + 2 * (i & 1)];
+              y[i] = fmaf(own, i & 1 ? pow2(20) : pow2(24), -less8) * f;
             }
-            if (g == 0) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(m[cg][j], sum);
+            if (whole) *reinterpret_cast<uint2*>(o + 32 * F * n) = make_uint2(wm_pack_bf16x2(y[0], y[1]), wm_pack_bf16x2(y[2], y[3]));
+            else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);
+          }
+          if (g == 0 && half == 0) {
+            if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(m[cg][j], sum);
+            else if (a.lse) a.lse[static_cast<size_t>(ub) * a.Sq * a.Hq + (uh * heads + o_at[cg][j] - tok[cg][j] * a.Hq) * a.Sq + tok[cg][j]] =
+                sum == 0.f ? -INFINITY : (m[cg][j] + log2f(sum)) * kLn2;
           }
         }
       }
+    if (!whole && lane == 0) segs[2 * warp + which] = Segment{ub, uu, starts, ends};
     which = 1;
   };
 
+  if (mine > 0) begin_unit(b0_, u0_, len0_);  // while the first stages are on their way
+  int slot = 0;
+  uint32_t phase = 0;
   while (consumed < produced) {
-    const int slot = static_cast<int>(consumed % R);
-    const bool mine = mbar_wait(&bars[slot], (consumed / R) & 1);
-    if (!__all_sync(0xffffffffu, mine)) {
+    const bool full = mbar_wait(&bars[slot], phase);
+    if (!__all_sync(0xffffffffu, full)) {
       ok = false;
       break;
     }
     const int4 md = meta[slot];
-    const int k0 = md.z & ~31, flags = md.z & 31, ulen = md.w;
+    const int k0 = md.z & -C::kKeys, flags = md.z & (C::kKeys - 1), ulen = md.w;
     if (flags & 1) {
-      begin_unit(md.x, md.y, ulen);
+      if (consumed) begin_unit(md.x, md.y, ulen);
       seg_k0 = k0;
     }
     const uint8_t* base = ring + slot * C::kStage;
-    const int bad = flags >> 2 & 3;
-    if (bad || k0 + kStageKeys > ulen - a.Sq + 1) stage(std::true_type{}, base, k0, bad, ulen - k0 > 16 ? 2 : 1);
-    else stage(std::false_type{}, base, k0, 0, 2);
+#pragma unroll 1
+    for (int i = 0; i < C::T && k0 + 16 * i < ulen; i += 2) two_tiles(base + i * C::kTile, k0 + 16 * i, flags >> (2 + i) & 3, ulen);
     __syncwarp();
     ++consumed;
     if (left > 0) {
       produce(slot);
       ++produced;
     }
-    if (flags & 2) end_unit(md.x, md.y, seg_k0 == 0 && k0 + kStageKeys >= ulen);
+    if (++slot == R) {
+      slot = 0;
+      phase ^= 1;
+    }
+    if (flags & 2) end_unit(md.x, md.y, seg_k0 == 0, k0 + C::kKeys >= ulen);
   }
   if (!ok) {
     if (lane == 0) atomicCAS(pg.err, 0, kErrDeviceTimeout);
     // every copy that this warp started lands before the CTA retires
-    for (uint32_t c = consumed; c < produced; ++c) mbar_wait(&bars[c % R], (c / R) & 1);
+    for (int c = consumed; c < produced; ++c) mbar_wait(&bars[c % R], (c / R) & 1);
+  }
+  __syncthreads();
+
+  // Segments of one unit follow one another in the warps' slots: join them, all units' columns at once.
+  Segment sg;
+  sg.b = -1;
+  if (lane < 2 * W) sg = segs[lane];
+  const unsigned valid = __ballot_sync(0xffffffffu, sg.b >= 0);
+  const unsigned firsts = __ballot_sync(0xffffffffu, sg.b >= 0 && sg.starts) | (valid & (0u - valid));
+  const unsigned endings = __ballot_sync(0xffffffffu, sg.b >= 0 && sg.ends);
+  const int items = cols.per * (D / 4);
+  int i0 = __ffs(firsts) - 1, passed = 0;  // the first segment of the unit at hand; units before it, times items
+  for (int at = threadIdx.x; firsts; at += W * 32) {
+    while (i0 >= 0 && at >= passed + items) {
+      passed += items;
+      i0 = __ffs(firsts & ~((2u << i0) - 1u)) - 1;
+    }
+    if (i0 < 0) break;
+    const unsigned later = firsts & ~((2u << i0) - 1u);
+    unsigned members = valid & ~((1u << i0) - 1u) & ((later & (0u - later)) - 1u);
+    const Segment first = segs[i0];
+    const bool ends = endings >> (31 - __clz(members)) & 1;
+    const int uh = first.u / cols.blocks, c0 = (first.u - uh * cols.blocks) * cols.per;
+    const int item = at - passed, c = item / (D / 4), ch = item % (D / 4) * 4, col = c0 + c;
+    if (col >= live_cols) continue;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, sum = 0.f;
+    while (members) {
+      constexpr int kBatch = 6;  // loads in flight
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (members) {
+          const float* from = my_slots + (__ffs(members) - 1) * C::kSlotFloats;
+          ml[i] = *reinterpret_cast<const float2*>(from + C::kCols * D + 2 * c);
+          v[i] = *reinterpret_cast<const float4*>(from + c * D + ch);
+          members &= members - 1;
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+      const float zero = top == -INFINITY ? 0.f : top, old = wm_ex2(M - zero);
+      M = top;
+      sum *= old;
+      O.x *= old, O.y *= old, O.z *= old, O.w *= old;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float wt = wm_ex2(ml[i].x - zero);
+        sum = fmaf(wt, ml[i].y, sum);
+        O.x = fmaf(wt, v[i].x, O.x), O.y = fmaf(wt, v[i].y, O.y), O.z = fmaf(wt, v[i].z, O.z), O.w = fmaf(wt, v[i].w, O.w);
+      }
+    }
+    if (first.starts && ends) {
+      const int hd = col / a.Sq, sq = col - hd * a.Sq, hq = uh * heads + hd;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + ((static_cast<size_t>(first.b) * a.Sq + sq) * a.Hq + hq) * D + ch) =
+          make_uint2(wm_pack_bf16x2(O.x * inv, O.y * inv), wm_pack_bf16x2(O.z * inv, O.w * inv));
+      if (ch == 0 && a.lse)
+        a.lse[(static_cast<size_t>(first.b) * a.Hq + hq) * a.Sq + sq] = sum == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(sum)) * kLn2;
+    } else {
+      // what leaves the CTA: slot 0 for the segment with the run's first stage, slot 1 for the one with its last
+      float* out = my_slots + (2 * W + (i0 == 0 ? 0 : 1)) * C::kSlotFloats;
+      *reinterpret_cast<float4*>(out + c * D + ch) = O;
+      if (ch == 0) *reinterpret_cast<float2*>(out + C::kCols * D + 2 * c) = make_float2(M, sum);
+    }
   }
 }
 
-template <int D, int NCG>
-__global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(const DecodeKv4Args a, const Columns cols, long long warps,
-                                                                            const long long* start, const float* slots) {
-  using C = Cfg<D, NCG>;
-  constexpr int kLanes = D / 4, kRows = kCombineThreads / kLanes;  // threads of a slot's row, rows at once
-  __shared__ float red[kCombineThreads / 32], sums[kRows];
-  __shared__ float4 part_o[kRows][kLanes];
-  const int row = blockIdx.x;  // [B, Sq, Hq]
-  const int hq = row % a.Hq, sq = row / a.Hq % a.Sq, b = row / a.Hq / a.Sq;
-  const int heads = a.Hq / a.pages.Hkv, units = a.pages.Hkv * cols.blocks;
-  const int col = hq % heads * a.Sq + sq, c = col % cols.per;
-  const int u = hq / heads * cols.blocks + col / cols.per;
+template <int D, int NCG, int F>
+__global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(const DecodeKv4Args a, const Columns cols, int ctas,
+                                                                            const Run* runs, const float* slots) {
+  using C = Cfg<D, NCG, F>;
+  __shared__ float4 part_o[kCombineThreads];
+  __shared__ float2 part_ml[kCombineThreads];
+  const int i = blockIdx.x + 1;  // the boundary before the run of CTA i
   const int tid = threadIdx.x;
   pdl_wait();  // the first kernel has finished and its slots are visible
-  Split sp;
-  sp.total = start[a.pages.B] * units;
-  sp.parts = sp.total < warps ? sp.total : warps;
-  const long long s0 = start[b];
-  const int nst = static_cast<int>(start[b + 1] - s0);
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + static_cast<size_t>(row) * D;
-  float* lse = a.lse ? a.lse + (static_cast<size_t>(b) * a.Hq + hq) * a.Sq + sq : nullptr;
-  if (nst == 0) {
-    if (tid < D) o[tid] = __float2bfloat16_rn(0.f);
-    if (tid == 0 && lse) *lse = -INFINITY;
-    return;
-  }
-  const long long first = s0 * units + static_cast<long long>(u) * nst;
-  const long long i0 = sp.part_of(first);
-  const int n = static_cast<int>(sp.part_of(first + nst - 1) - i0) + 1;
-  if (n == 1) return;  // one warp had the whole unit and has written it
-  // The unit's first part may have begun in an earlier unit; it is then that warp's second slot.
-  const int late = sp.first(i0) < first ? 1 : 0;
-  auto slot = [&](int i) { return slots + (2 * (i0 + i) + (i == 0 ? late : 0)) * C::kSlotFloats; };
-  float M = -INFINITY;
-  for (int i = tid; i < n; i += kCombineThreads) M = fmaxf(M, slot(i)[C::kCols * D + 2 * c]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if ((tid & 31) == 0) red[tid >> 5] = M;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kCombineThreads / 32; ++i) M = fmaxf(M, red[i]);
-  if (M == -INFINITY) M = 0.f;  // nothing seen, or NaN: weights 0
-  const int r = tid / kLanes, ch = tid % kLanes;
+  const Run run = runs[i];
+  const long long total = runs[ctas].x, before = runs[i - 1].x;
+  // The unit at the boundary starts at stage `first`; the boundary is the unit's first one, or another CTA's.
+  const long long first = run.x - run.st;
+  if (run.x >= total || run.st == 0 || first < before) return;
+  // It has parts in CTA i - 1 and in every later one that starts inside it.
+  const int n = 1 + __syncthreads_count(tid + i < ctas && runs[min(tid + i, ctas)].x < first + run.nst);
+  const int late = before < first ? 1 : 0;
+  const int heads = a.Hq / a.pages.Hkv, live_cols = heads * a.Sq;
+  const int uh = run.u / cols.blocks, c0 = (run.u - uh * cols.blocks) * cols.per;
+  const int items = cols.per * (D / 4), rows = kCombineThreads / items;
+  const int item = tid % items, r = tid / items;
+  const int c = item / (D / 4), ch = item % (D / 4) * 4;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  float W = 0.f;
+  float M = -INFINITY, sum = 0.f;
+  if (r < rows && c0 + c < live_cols) {
 #pragma unroll 4
-  for (int i = r; i < n; i += kRows) {
-    const float* s = slot(i);
-    const float2 ml = *reinterpret_cast<const float2*>(s + C::kCols * D + 2 * c);
-    const float4 x = *reinterpret_cast<const float4*>(s + c * D + 4 * ch);
-    const float w = wm_ex2(ml.x - M);
-    W = fmaf(w, ml.y, W);
-    O.x = fmaf(w, x.x, O.x), O.y = fmaf(w, x.y, O.y), O.z = fmaf(w, x.z, O.z), O.w = fmaf(w, x.w, O.w);
-  }
-  part_o[r][ch] = O;
-  if (ch == 0) sums[r] = W;
-  __syncthreads();
-  if (tid < D) {
-    float num = 0.f;
-    W = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      num += reinterpret_cast<const float*>(part_o[i])[tid];
-      W += sums[i];
+    for (int k = r; k < n; k += rows) {
+      const float* from = slots + (static_cast<size_t>(i - 1 + k) * C::kSlots + 2 * C::W + (k == 0 ? late : 0)) * C::kSlotFloats;
+      const float2 ml = *reinterpret_cast<const float2*>(from + C::kCols * D + 2 * c);
+      const float4 v = *reinterpret_cast<const float4*>(from + c * D + ch);
+      const float top = fmaxf(M, ml.x), zero = top == -INFINITY ? 0.f : top;
+      const float old = wm_ex2(M - zero), wt = wm_ex2(ml.x - zero);
+      M = top;
+      sum = fmaf(wt, ml.y, sum * old);
+      O.x = fmaf(wt, v.x, O.x * old), O.y = fmaf(wt, v.y, O.y * old), O.z = fmaf(wt, v.z, O.z * old), O.w = fmaf(wt, v.w, O.w * old);
     }
-    o[tid] = __float2bfloat16_rn(W == 0.f ? 0.f : num / W);
-    if (tid == 0 && lse) *lse = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
   }
+  part_o[tid] = O;
+  part_ml[tid] = make_float2(M, sum);
+  __syncthreads();
+  if (r > 0 || c0 + c >= live_cols) return;
+  float top = M;
+  for (int k = 1; k < rows; ++k) top = fmaxf(top, part_ml[k * items + item].x);
+  const float zero = top == -INFINITY ? 0.f : top;
+  O = make_float4(0.f, 0.f, 0.f, 0.f);
+  sum = 0.f;
+  for (int k = 0; k < rows; ++k) {
+    const float2 ml = part_ml[k * items + item];
+    const float4 v = part_o[k * items + item];
+    const float wt = wm_ex2(ml.x - zero);
+    sum = fmaf(wt, ml.y, sum);
+    O.x = fmaf(wt, v.x, O.x), O.y = fmaf(wt, v.y, O.y), O.z = fmaf(wt, v.z, O.z), O.w = fmaf(wt, v.w, O.w);
+  }
+  const int col = c0 + c, hq = uh * heads + col / a.Sq, sq = col % a.Sq;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + ((static_cast<size_t>(run.b) * a.Sq + sq) * a.Hq + hq) * D + ch) =
+      make_uint2(wm_pack_bf16x2(O.x * inv, O.y * inv), wm_pack_bf16x2(O.z * inv, O.w * inv));
+  if (ch == 0 && a.lse) a.lse[(static_cast<size_t>(run.b) * a.Hq + hq) * a.Sq + sq] = sum == 0.f ? -INFINITY : (zero + log2f(sum)) * kLn2;
 }
 
 Columns columns_of(int G, int Sq) {
@@ -599,63 +867,73 @@ Columns columns_of(int G, int Sq) {
   return {blocks, (n + blocks - 1) / blocks};
 }
 
-size_t header_bytes(int B) { return (static_cast<size_t>(B + 1) * sizeof(long long) + 255) / 256 * 256; }
+constexpr size_t kRunsBytes = (kMaxCtas + 1) * sizeof(Run);
+static_assert(kRunsBytes % 16 == 0 && sizeof(Run) == 32, "slots start 16-byte aligned");
 
-long long most_parts(int B, int units, long long max_tokens, int warps) {
-  const double most = static_cast<double>(B) * units * static_cast<double>((max_tokens + kStageKeys - 1) / kStageKeys);
-  const long long parts = static_cast<long long>(kMaxCtas) * warps;
-  return most < static_cast<double>(parts) ? static_cast<long long>(most) : parts;
+// CTAs of a call: one per SM, fewer where even the longest sequences have fewer stages.
+int ctas_of(int B, int units, long long max_tokens, int keys) {
+  const double most = static_cast<double>(B) * units * static_cast<double>((max_tokens + keys - 1) / keys);
+  return most < kMaxCtas ? static_cast<int>(most) : kMaxCtas;
 }
 
-template <int D, int NCG>
+template <int D, int NCG, int F>
 size_t workspace_of(int B, int units, long long max_tokens) {
-  using C = Cfg<D, NCG>;
-  return header_bytes(B) + 2 * static_cast<size_t>(most_parts(B, units, max_tokens, C::W)) * C::kSlotFloats * sizeof(float);
+  using C = Cfg<D, NCG, F>;
+  return kRunsBytes + static_cast<size_t>(ctas_of(B, units, max_tokens, C::kKeys)) * C::kSlots * C::kSlotFloats * sizeof(float);
 }
 
-template <int D, int NCG>
+template <int D, int NCG, int F>
 cudaError_t launch_dn(const Columns cols, const DecodeKv4Args& a, cudaStream_t s) {
-  using C = Cfg<D, NCG>;
-  static_assert(C::kSmem <= 227 * 1024 && C::R >= 3, "the rings of all warps fit one SM");
+  using C = Cfg<D, NCG, F>;
+  static_assert(C::kSmem <= 227 * 1024 && C::R >= 2 && 2 * C::W <= 32, "the rings of all warps fit one SM");
   static DeviceOnce attr_set;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!attr_set.test(dev)) {
-    e = cudaFuncSetAttribute(decode_kv4_kernel<D, NCG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(decode_kv4_kernel<D, NCG, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set.set(dev);
   }
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const Kv4Pages& p = a.pages;
-  const int units = p.Hkv * cols.blocks;
-  const long long parts = most_parts(p.B, units, static_cast<long long>(p.max_pages) << p.page_shift, C::W);
-  int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  if (parts < grid) grid = static_cast<int>(parts);
-  long long* start = static_cast<long long*>(a.work);
-  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(a.work) + header_bytes(p.B));
-  decode_kv4_kernel<D, NCG><<<grid, C::W * 32, C::kSmem, s>>>(a, cols, start, slots);
+  const int most = ctas_of(p.B, p.Hkv * cols.blocks, static_cast<long long>(p.max_pages) << p.page_shift, C::kKeys);
+  const int grid = most < sms ? most : sms;
+  Run* runs = static_cast<Run*>(a.work);
+  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(a.work) + kRunsBytes);
+  decode_kv4_kernel<D, NCG, F><<<grid, C::W * 32, C::kSmem, s>>>(a, cols, runs, slots);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_after_pdl(decode_kv4_combine_kernel<D, NCG>, dim3(static_cast<unsigned>(p.B) * a.Sq * a.Hq), dim3(kCombineThreads), 0, s, a,
-                          cols, static_cast<long long>(grid) * C::W, static_cast<const long long*>(start), static_cast<const float*>(slots));
+  if (e != cudaSuccess || grid == 1) return e;
+  return launch_after_pdl(decode_kv4_combine_kernel<D, NCG, F>, dim3(grid - 1), dim3(kCombineThreads), 0, s, a, cols, grid,
+                          static_cast<const Run*>(runs), static_cast<const float*>(slots));
+}
+
+// The columns (query head, token) of a KV head's group decide the form.  Up to 4 fill half an MMA and share it
+// between two groups of channels; up to 8 fill one; up to 16 two.
+template <typename Fn>
+auto with_form(int d, int per, Fn fn) {
+  using std::integral_constant;
+  if (d == 64) {
+    if (per <= 4) return fn(integral_constant<int, 64>{}, integral_constant<int, 1>{}, integral_constant<int, 2>{});
+    if (per <= 8) return fn(integral_constant<int, 64>{}, integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    return fn(integral_constant<int, 64>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  }
+  if (per <= 4) return fn(integral_constant<int, 128>{}, integral_constant<int, 1>{}, integral_constant<int, 2>{});
+  if (per <= 8) return fn(integral_constant<int, 128>{}, integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  return fn(integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
 }
 
 }  // namespace
 
-// One group of 8 MMA columns where the (query head, token) pairs of a KV head fit it, two otherwise.
 size_t decode_kv4_workspace_bytes(int B, int Sq, int Hq, int Hkv, long long max_tokens, int d) {
   const Columns c = columns_of(Hq / Hkv, Sq);
-  const int units = Hkv * c.blocks;
-  if (d == 64) return c.per <= 8 ? workspace_of<64, 1>(B, units, max_tokens) : workspace_of<64, 2>(B, units, max_tokens);
-  return c.per <= 8 ? workspace_of<128, 1>(B, units, max_tokens) : workspace_of<128, 2>(B, units, max_tokens);
+  return with_form(d, c.per, [&](auto D, auto NCG, auto F) { return workspace_of<D(), NCG(), F()>(B, Hkv * c.blocks, max_tokens); });
 }
 
 cudaError_t launch_decode_kv4(int d, const DecodeKv4Args& a, cudaStream_t s) {
   const Columns c = columns_of(a.Hq / a.pages.Hkv, a.Sq);
-  if (d == 64) return c.per <= 8 ? launch_dn<64, 1>(c, a, s) : launch_dn<64, 2>(c, a, s);
-  return c.per <= 8 ? launch_dn<128, 1>(c, a, s) : launch_dn<128, 2>(c, a, s);
+  return with_form(d, c.per, [&](auto D, auto NCG, auto F) { return launch_dn<D(), NCG(), F()>(c, a, s); });
 }
 
 }  // namespace eio
