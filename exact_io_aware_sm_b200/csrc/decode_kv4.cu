@@ -72,7 +72,7 @@ struct Cfg {
   static constexpr int kSmem = kOffSegs + 2 * W * 16;
   static constexpr int kCols = 8 * NCG / F;
   static constexpr int kSlotFloats = kCols * (D + 2);  // numerators [col][D], then (maximum, sum) [col]
-  static constexpr int kSlots = 2 * W + 2;             // of a CTA: two a warp, two for what leaves the CTA
+  static constexpr int kSlots = W + 2;                 // of a CTA: one a warp, two for what leaves the CTA
 };
 
 // Where the run of a CTA starts: stage x of all, stage st (of nst) of unit u of sequence b.
@@ -84,8 +84,9 @@ struct Run {
 
 // A segment (the part of a unit in a warp's run) that is not a whole unit.
 struct Segment {
-  int b, u;   // b < 0: none
-  int starts, ends;
+  int b, u;  // b < 0: none
+  int ends;  // bit 0: with the unit's first stage, bit 1: with its last
+  int near;  // its results are in the warp's ring, else in its slot
 };
 
 __device__ __forceinline__ int checked_len(const Kv4Pages& p, int b) {
@@ -146,6 +147,12 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Products of two bf16 pairs.
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {
+  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -246,6 +253,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     }
   }
 
+  int consumed = 0;
   bool fresh = true;           // the next stage is its run's first of a unit
   int win = 0, ids = 0;        // lane i holds the page id of page win + i of sequence b
   int win_end = 0;             // 0: no such window yet
@@ -334,11 +342,6 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     if (lane == 0) meta[slot] = make_int4(b, h * cols.blocks + cb, k0 | flags, len);
   };
 
-  const int b0_ = b, u0_ = h * cols.blocks + cb, len0_ = len;
-  int produced = 0, consumed = 0;
-  for (; produced < R && left > 0; ++produced) produce(produced);
-  __syncwarp();
-
   // Columns.  An MMA has 8; with F = 2 the upper four repeat the lower four for the odd groups (of a pair
   // of groups), so that one accumulator holds both groups' sums and a lane scales only its own group's.  This lane:
   // column g as a row of q (and of the B operands), columns 2 t and 2 t + 1 of the accumulators.
@@ -354,13 +357,17 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   int vis[NCG][2];                // keys that the column sees
   float acc[NCG][G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and + 1: 16 times as large), columns 2 t, 2 t + 1
   float psum[NCG][NS][4];         // 8 sum of P sv, as rounded: columns 2 t and 2 t + 1, twice
-  float m[NCG][2], l[NCG][2];
+  float m[NCG][2], l[NCG][2];     // maximum (in log2 units, as of the last move of the base) and sum
+  float mneg[NCG][2];             // -m, or 0 in a column that has seen no key yet (its p are 0)
+  float limit[NCG][2];            // a raw score above this moves the base
   float rinv[NS];                 // P sv goes in times this: 2^6 over the reference of the lane's group
   uint32_t ref[G / 2];            // the references as bf16, packed like the scales
+  uint32_t my_ref;                // ref[t % (G / 2)]: the lane checks that word of one row in four lanes' turn
   int seg_k0 = 0, which = 0;
   bool ok = true;
 
-  auto begin_unit = [&](int ub, int uu, int ulen) {
+  uint4 raw[NCG][G];              // q as read
+  auto read_q = [&](int ub, int uu) {
     const int uh = cols.blocks == 1 ? uu : uu / cols.blocks, ucb = uu - uh * cols.blocks;
     if (ucb != at_cb) {
       at_cb = ucb;
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           const int c = (cg * 8 + (j < 2 ? 2 * t + j : g)) & (C::kCols - 1), col = ucb * cols.per + c;
-          const int hd = col / a.Sq, tk = col - hd * a.Sq;
+          const int hd = a.Sq == 1 ? col : col / a.Sq, tk = col - hd * a.Sq;
           const int at = c < cols.per && col < live_cols ? tk * a.Hq + hd : -1;
           if (j < 2) {
             o_at[cg][j] = at;
@@ -384,57 +391,57 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     for (int cg = 0; cg < NCG; ++cg) {
       const bool live = q_at[cg] >= 0;
       const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) + (row0 + (live ? q_at[cg] : 0)) * D + 8 * t;
-      uint4 raw[G];
 #pragma unroll
-      for (int grp = 0; grp < G; ++grp) raw[grp] = live ? *reinterpret_cast<const uint4*>(row + 32 * grp) : make_uint4(0u, 0u, 0u, 0u);
+      for (int grp = 0; grp < G; ++grp) raw[cg][grp] = live ? *reinterpret_cast<const uint4*>(row + 32 * grp) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  auto begin_unit = [&](int ulen) {
+#pragma unroll
+    for (int cg = 0; cg < NCG; ++cg) {
       uint32_t mx = 0;
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) {
-        const uint32_t w[4] = {raw[grp].x, raw[grp].y, raw[grp].z, raw[grp].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+        const uint4 w = raw[cg][grp];
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
       }
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int e = min(max(141 - static_cast<int>(mx >> 7), -100), 100);  // q 2^e
-      const float up = pow2(e), fc = a.scale_log2 * pow2(24 - e);
-      float sums[G];
+      const float fc = a.scale_log2 * pow2(24 - e);
+      // Codes n and n + 4 of a word sit 16 bits apart; odd n are masked 4 bits higher, 16 times as large.
+      const uint32_t up = static_cast<uint32_t>(127 + e) << 7 | static_cast<uint32_t>(123 + e) << 23;  // bf16 2^e, 2^(e - 4)
+      float x0 = 0.f, x1 = 0.f;
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) {
-        const uint32_t w[4] = {raw[grp].x, raw[grp].y, raw[grp].z, raw[grp].w};
-        float x[8], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[2 * i] = __uint_as_float(w[i] << 16) * up;
-          x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * up;
-        }
-        // codes (n, n + 4) of a word sit 16 bits apart; odd n are masked 4 bits higher, 16 times as large
+        const uint32_t y[4] = {times(raw[cg][grp].x, up), times(raw[cg][grp].y, up), times(raw[cg][grp].z, up), times(raw[cg][grp].w, up)};
+        const bool mine = F == 1 || half_q == (grp & 1);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const float f = n & 1 ? 1.f / 16.f : 1.f;
-          const __half2 v = __floats2half2_rn(x[n] * f, x[n + 4] * f);
-          qf[cg][grp][n] = F == 1 || half_q == (grp & 1) ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
-          const float2 back = __half22float2(v);
-          sum += (back.x + back.y) * (n & 1 ? 16.f : 1.f);
+          const uint32_t v = __byte_perm(y[n >> 1], y[2 + (n >> 1)], n & 1 ? 0x7632 : 0x5410);
+          qf[cg][grp][n] = mine ? pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)) : 0u;
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sums[grp] = sum * (-8.f * pow2(-24));
+        // 8 sum q of the columns, by an MMA; -8 sum q of this lane's column g in the two groups of its k
+        const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00800080u, 0x00800080u};
+        float d[4];
+        mma_f16_first(d, eights, qf[cg][grp][0], qf[cg][grp][1]);
+        mma_f16(d, eights, qf[cg][grp][2], qf[cg][grp][3]);
+        const int pc = F == 2 ? (g & 3) + 4 * (grp & 1) : g;
+        const float d0 = __shfl_sync(0xffffffffu, d[0], pc >> 1), d1 = __shfl_sync(0xffffffffu, d[1], pc >> 1);
+        const float sum = pc & 1 ? -d1 : -d0;
+        if (G == 2 || (grp >> 1) == (t & 1)) {
+          if (grp & 1) x1 = sum;
+          else x0 = sum;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[cg][grp][0][i] = acc[cg][grp][1][i] = psum[cg][grp / F][i] = 0.f;
       }
       // Row k of this operand is part k / G of group k % G (d = 128: parts 0 and 1 in b0, 2 and 3 in b1;
       // d = 64: 0 to 3 in b0), so that a row of K's scales, repeated, is the other operand.
-      float x0 = sums[0], x1 = sums[1];
-      if constexpr (G == 4) {
-        if (t & 1) x0 = sums[2], x1 = sums[3];
-      }
       uint32_t parts[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-        parts[i] = half_q ? 0u : *reinterpret_cast<const uint32_t*>(&h);
+        parts[i] = half_q ? 0u : wm_pack_bf16x2(x0, x1);
         x0 -= __uint_as_float(parts[i] << 16);
         x1 -= __uint_as_float(parts[i] & 0xffff0000u);
       }
@@ -449,15 +456,22 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
       for (int j = 0; j < 2; ++j) {
         fac[cg][j] = __shfl_sync(0xffffffffu, fc, (2 * t + j) * 4);
         vis[cg][j] = ulen - a.Sq + 1 + tok[cg][j];
-        m[cg][j] = -INFINITY;
-        l[cg][j] = 0.f;
+        m[cg][j] = limit[cg][j] = -INFINITY;
+        mneg[cg][j] = l[cg][j] = 0.f;
       }
     }
 #pragma unroll
     for (int i = 0; i < G / 2; ++i) ref[i] = 0;
+    my_ref = 0;
 #pragma unroll
     for (int i = 0; i < NS; ++i) rinv[i] = pow2(106);
   };
+
+  const int first_len = len;
+  if (mine > 0) read_q(b, h * cols.blocks + cb);
+  int produced = 0;
+  for (; produced < R && left > 0; ++produced) produce(produced);
+  __syncwarp();
 
   // This lane's scale of set n (its group, or the lane's one of its pair) among packed scales.
   auto scale_at = [&](const uint32_t* w, int n) -> float {
@@ -496,12 +510,13 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         ref[grp >> 1] = grp & 1 ? (ref[grp >> 1] & 0xffffu) | bits << 16 : (ref[grp >> 1] & 0xffff0000u) | bits;
       }
     }
+    my_ref = t % (G / 2) ? ref[G / 2 - 1] : ref[0];
   };
 
   // Two tiles of a stage: keys k0 .. k0 + 31; bit i of bad: the page of tile i is missing.
   auto two_tiles = [&](const uint8_t* base, int k0, int bad, int ulen) {
     float s[2][NCG][4];
-    uint32_t vs[2][2][G / 2], top[G / 2] = {};
+    uint32_t vs[2][2][G / 2], check[2];
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       const uint8_t* p = base + tile * C::kTile;
@@ -515,6 +530,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
       const uint32_t lo = *reinterpret_cast<const uint32_t*>(p + kv4_off_ks(D) + g * (2 * G) + (t % (G / 2)) * 4);
       const uint32_t hi = *reinterpret_cast<const uint32_t*>(p + kv4_off_ks(D) + (g + 8) * (2 * G) + (t % (G / 2)) * 4);
       const uint32_t sc[4] = {lo, hi, lo, hi};
+      check[tile] = *reinterpret_cast<const uint32_t*>(p + kv4_off_vs(D) + (g + 8 * (t >> 1)) * (2 * G) + (t % (G / 2)) * 4);
 #pragma unroll
       for (int cg = 0; cg < NCG; ++cg) mma_bf16_first(s[tile][cg], sc, less[cg][0], less[cg][1]);
       float raw[NCG][4];
@@ -540,7 +556,8 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         for (int i = 0; i < 4; ++i) s[tile][0][i] += __shfl_xor_sync(0xffffffffu, s[tile][0][i], 2);
       }
     }
-    if (bad || k0 + 32 > ulen - a.Sq + 1) {  // some key is past a column's last one, or its page is missing
+    const bool edge = bad || k0 + 32 > ulen - a.Sq + 1;
+    if (edge) {  // some key is past a column's last one, or its page is missing
       uint32_t odd = 0;                       // V scales that are not finite, of keys that are there
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
@@ -582,38 +599,45 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
           }
       }
     }
-#pragma unroll
-    for (int i = 0; i < G / 2; ++i) top[i] = __vmaxu2(__vmaxu2(vs[0][0][i], vs[0][1][i]), __vmaxu2(vs[1][0][i], vs[1][1][i]));
-    bool over = false;
-#pragma unroll
-    for (int i = 0; i < G / 2; ++i) over |= __vmaxu2(top[i], ref[i]) != ref[i];
-    if (__any_sync(0xffffffffu, over)) move_refs(vs);
-    float mneg[NCG][2];
+    // The base and the references move seldom: only then are the column's maximum and the largest scales looked for.
+    float high[NCG][2];
+    bool moves = edge || __vmaxu2(__vmaxu2(check[0], check[1]), my_ref) != my_ref;
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float v = fmaxf(fmaxf(s[0][cg][j], s[0][cg][j + 2]), fmaxf(s[1][cg][j], s[1][cg][j + 2]));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        v *= fac[cg][j];
-        if (v > m[cg][j] + kRebase) {
-          const float alpha = wm_ex2(m[cg][j] - v);
-          l[cg][j] *= alpha;
-#pragma unroll
-          for (int grp = 0; grp < G; ++grp)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              acc[cg][grp][i][j] *= alpha;
-              acc[cg][grp][i][j + 2] *= alpha;
-            }
-#pragma unroll
-          for (int n = 0; n < NS; ++n) psum[cg][n][j] *= alpha;
-          m[cg][j] = v;
-        }
-        mneg[cg][j] = m[cg][j] == -INFINITY ? 0.f : -m[cg][j];  // a column that has seen no key yet: its p are 0
+        high[cg][j] = fmaxf(fmaxf(s[0][cg][j], s[0][cg][j + 2]), fmaxf(s[1][cg][j], s[1][cg][j + 2]));
+        moves |= high[cg][j] > limit[cg][j];
       }
+    if (__any_sync(0xffffffffu, moves)) {
+      move_refs(vs);
+#pragma unroll
+      for (int cg = 0; cg < NCG; ++cg)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v = high[cg][j];
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          v *= fac[cg][j];
+          if (v > m[cg][j] + kRebase) {
+            const float alpha = wm_ex2(m[cg][j] - v);
+            l[cg][j] *= alpha;
+#pragma unroll
+            for (int grp = 0; grp < G; ++grp)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                acc[cg][grp][i][j] *= alpha;
+                acc[cg][grp][i][j + 2] *= alpha;
+              }
+#pragma unroll
+            for (int n = 0; n < NS; ++n) psum[cg][n][j] *= alpha;
+            m[cg][j] = v;
+            mneg[cg][j] = -v;
+            limit[cg][j] = __fdividef(v + kRebase, fac[cg][j]);
+          }
+        }
+    }
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       const uint8_t* p = base + tile * C::kTile;
@@ -657,8 +681,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   auto end_unit = [&](int ub, int uu, bool starts, bool ends) {
     const int uh = cols.blocks == 1 ? uu : uu / cols.blocks;
     const size_t row0 = static_cast<size_t>(ub) * a.Sq * a.Hq + uh * heads;
-    float* slot = my_slots + (2 * warp + which) * C::kSlotFloats;
     const bool whole = starts && ends;
+    // The run's last segment goes to the ring, which is free by then.
+    const bool near = consumed == produced;
+    float* slot = near ? reinterpret_cast<float*>(ring) : my_slots + warp * C::kSlotFloats;
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
@@ -692,11 +718,11 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
           }
         }
       }
-    if (!whole && lane == 0) segs[2 * warp + which] = Segment{ub, uu, starts, ends};
+    if (!whole && lane == 0) segs[2 * warp + which] = Segment{ub, uu, starts | ends << 1, near};
     which = 1;
   };
 
-  if (mine > 0) begin_unit(b0_, u0_, len0_);  // while the first stages are on their way
+  if (mine > 0) begin_unit(first_len);  // while the first stages are on their way
   int slot = 0;
   uint32_t phase = 0;
   while (consumed < produced) {
@@ -708,7 +734,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     const int4 md = meta[slot];
     const int k0 = md.z & -C::kKeys, flags = md.z & (C::kKeys - 1), ulen = md.w;
     if (flags & 1) {
-      if (consumed) begin_unit(md.x, md.y, ulen);
+      if (consumed) {
+        read_q(md.x, md.y);
+        begin_unit(ulen);
+      }
       seg_k0 = k0;
     }
     const uint8_t* base = ring + slot * C::kStage;
@@ -738,8 +767,9 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   sg.b = -1;
   if (lane < 2 * W) sg = segs[lane];
   const unsigned valid = __ballot_sync(0xffffffffu, sg.b >= 0);
-  const unsigned firsts = __ballot_sync(0xffffffffu, sg.b >= 0 && sg.starts) | (valid & (0u - valid));
-  const unsigned endings = __ballot_sync(0xffffffffu, sg.b >= 0 && sg.ends);
+  const unsigned firsts = __ballot_sync(0xffffffffu, sg.b >= 0 && (sg.ends & 1)) | (valid & (0u - valid));
+  const unsigned near = __ballot_sync(0xffffffffu, sg.b >= 0 && sg.near);
+  const unsigned endings = __ballot_sync(0xffffffffu, sg.b >= 0 && (sg.ends & 2));
   const int items = cols.per * (D / 4);
   int i0 = __ffs(firsts) - 1, passed = 0;  // the first segment of the unit at hand; units before it, times items
   for (int at = threadIdx.x; firsts; at += W * 32) {
@@ -766,7 +796,8 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         ml[i] = make_float2(-INFINITY, 0.f);
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (members) {
-          const float* from = my_slots + (__ffs(members) - 1) * C::kSlotFloats;
+          const int x = __ffs(members) - 1;
+          const float* from = near >> x & 1 ? reinterpret_cast<const float*>(smem + (x >> 1) * R * C::kStage) : my_slots + (x >> 1) * C::kSlotFloats;
           ml[i] = *reinterpret_cast<const float2*>(from + C::kCols * D + 2 * c);
           v[i] = *reinterpret_cast<const float4*>(from + c * D + ch);
           members &= members - 1;
@@ -786,7 +817,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         O.x = fmaf(wt, v[i].x, O.x), O.y = fmaf(wt, v[i].y, O.y), O.z = fmaf(wt, v[i].z, O.z), O.w = fmaf(wt, v[i].w, O.w);
       }
     }
-    if (first.starts && ends) {
+    if ((first.ends & 1) && ends) {
       const int hd = col / a.Sq, sq = col - hd * a.Sq, hq = uh * heads + hd;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + ((static_cast<size_t>(first.b) * a.Sq + sq) * a.Hq + hq) * D + ch) =
@@ -795,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         a.lse[(static_cast<size_t>(first.b) * a.Hq + hq) * a.Sq + sq] = sum == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(sum)) * kLn2;
     } else {
       // what leaves the CTA: slot 0 for the segment with the run's first stage, slot 1 for the one with its last
-      float* out = my_slots + (2 * W + (i0 == 0 ? 0 : 1)) * C::kSlotFloats;
+      float* out = my_slots + (W + (i0 == 0 ? 0 : 1)) * C::kSlotFloats;
       *reinterpret_cast<float4*>(out + c * D + ch) = O;
       if (ch == 0) *reinterpret_cast<float2*>(out + C::kCols * D + 2 * c) = make_float2(M, sum);
     }
@@ -829,7 +860,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(con
   if (r < rows && c0 + c < live_cols) {
 #pragma unroll 4
     for (int k = r; k < n; k += rows) {
-      const float* from = slots + (static_cast<size_t>(i - 1 + k) * C::kSlots + 2 * C::W + (k == 0 ? late : 0)) * C::kSlotFloats;
+      const float* from = slots + (static_cast<size_t>(i - 1 + k) * C::kSlots + C::W + (k == 0 ? late : 0)) * C::kSlotFloats;
       const float2 ml = *reinterpret_cast<const float2*>(from + C::kCols * D + 2 * c);
       const float4 v = *reinterpret_cast<const float4*>(from + c * D + ch);
       const float top = fmaxf(M, ml.x), zero = top == -INFINITY ? 0.f : top;
@@ -885,7 +916,7 @@ size_t workspace_of(int B, int units, long long max_tokens) {
 template <int D, int NCG, int F>
 cudaError_t launch_dn(const Columns cols, const DecodeKv4Args& a, cudaStream_t s) {
   using C = Cfg<D, NCG, F>;
-  static_assert(C::kSmem <= 227 * 1024 && C::R >= 2 && 2 * C::W <= 32, "the rings of all warps fit one SM");
+  static_assert(C::kSmem <= 227 * 1024 && C::R >= 2 && 2 * C::W <= 32 && C::R * C::kStage >= C::kSlotFloats * 4, "the rings of all warps fit one SM");
   static DeviceOnce attr_set;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
