@@ -69,13 +69,20 @@ struct Cfg {
   static constexpr int kOffMeta = W * R * kStage;
   static constexpr int kOffBars = kOffMeta + W * R * 16;
   static constexpr int kOffSegs = kOffBars + W * R * 8;
-  static constexpr int kSmem = kOffSegs + 2 * W * 16;
+  static constexpr int kSmem = kOffSegs + 2 * W * 16 + 16;
   static constexpr int kCols = 8 * NCG / F;
   static constexpr int kSlotFloats = kCols * (D + 2);  // numerators [col][D], then (maximum, sum) [col]
   static constexpr int kSlots = W + 2;                 // of a CTA: one a warp, two for what leaves the CTA
 };
 
-// Where the run of a CTA starts: stage x of all, stage st (of nst) of unit u of sequence b.
+// What a unit of len keys is counted for when the runs are cut: its stages and one more for its start and end
+// (the queries' fragments, the results), which cost about as much; nothing where there are no keys.
+template <int KEYS>
+__device__ __forceinline__ int cost_of(int len) {
+  return len > 0 ? (len + KEYS - 1) / KEYS + 1 : 0;
+}
+
+// Where the run of a CTA starts: at cost x of all, stage st (of nst) of unit u of sequence b.
 struct Run {
   long long x;
   int b, u, st, nst;
@@ -174,6 +181,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * R;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBars) + warp * R;
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kOffSegs);
+  int2* first_unit = reinterpret_cast<int2*>(segs + 2 * W);  // the unit that the CTA's run starts in
   const int units = pg.Hkv * cols.blocks;
   const int heads = a.Hq / pg.Hkv, live_cols = heads * a.Sq;
   const int tiles_shift = pg.page_shift - 4;
@@ -189,8 +197,8 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
 
   // The stages of the call, cut for the CTAs and then for the warps of each.
   const int len0 = lane < pg.B ? checked_len(pg, lane) : 0;  // of the first 32 sequences
-  long long total = (len0 + C::kKeys - 1) / C::kKeys;
-  for (int b = lane + 32; b < pg.B; b += 32) total += (checked_len(pg, b) + C::kKeys - 1) / C::kKeys;
+  long long total = cost_of<C::kKeys>(len0);
+  for (int b = lane + 32; b < pg.B; b += 32) total += cost_of<C::kKeys>(checked_len(pg, b));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   total *= units;
@@ -203,15 +211,15 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   const unsigned more_w = static_cast<unsigned>(n_cta - each_w * W);
   const long long x0 = cta_x + each_w * warp + min(static_cast<unsigned>(warp), more_w);
   int left = static_cast<int>(each_w + (warp < more_w));  // stages still to be produced
-  const int mine = left;
+  const bool any = left > 0;
 
   // The producer's place: stage st (of nst) of column block cb of KV head h of sequence b.
   int b = 0, h = 0, cb = 0, st = 0, nst = 0, len = 0;
-  if (mine > 0) {
-    long long base = 0;  // stages of a KV head before this group of 32 sequences
+  if (any) {
+    long long base = 0;  // costs of a KV head's units before this group of 32 sequences
     for (int c = 0; c < pg.B; c += 32) {
       const int l = c == 0 ? len0 : c + lane < pg.B ? checked_len(pg, c + lane) : 0;
-      const int n = (l + C::kKeys - 1) / C::kKeys;
+      const int n = cost_of<C::kKeys>(l);
       long long pre = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -224,10 +232,15 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         const int src = __ffs(past) - 1;
         b = c + src;
         len = __shfl_sync(0xffffffffu, l, src);
-        nst = __shfl_sync(0xffffffffu, n, src);
-        const long long in = x0 - (__shfl_sync(0xffffffffu, pre, src) - nst) * units;
-        const int u = static_cast<int>(in >> 32 ? in / nst : static_cast<unsigned>(in) / static_cast<unsigned>(nst));
-        st = static_cast<int>(in - static_cast<long long>(u) * nst);
+        const int cost = __shfl_sync(0xffffffffu, n, src);
+        const long long in = x0 - (__shfl_sync(0xffffffffu, pre, src) - cost) * units;
+        const int u = static_cast<int>(in >> 32 ? in / cost : static_cast<unsigned>(in) / static_cast<unsigned>(cost));
+        nst = cost - 1;
+        st = static_cast<int>(in - static_cast<long long>(u) * cost) - 1;
+        if (st < 0) {  // the unit's start, which is no stage
+          st = 0;
+          --left;
+        }
         h = u / cols.blocks;
         cb = u - h * cols.blocks;
         break;
@@ -238,6 +251,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   if (warp == 0 && lane == 0) {
     runs[cta] = Run{cta_x, b, h * cols.blocks + cb, st, nst, 0};
     if (cta + 1 == ctas) runs[ctas].x = total;
+    *first_unit = make_int2(b, h * cols.blocks + cb);
   }
   if (warp == W - 1) {  // sequences without a token are shared out among the CTAs
     for (int b0 = cta; b0 < pg.B; b0 += 32 * ctas) {
@@ -338,6 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     --left;
     ++st;
     const int flags = (fresh ? 1 : 0) | (st == nst || left == 0 ? 2 : 0) | bad << 2;
+    if (st == nst && left > 0) --left;  // the next unit's start
     fresh = false;
     if (lane == 0) meta[slot] = make_int4(b, h * cols.blocks + cb, k0 | flags, len);
   };
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   float fac[NCG][2];              // a raw score times this is the score in log2 units
   int vis[NCG][2];                // keys that the column sees
   float acc[NCG][G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and + 1: 16 times as large), columns 2 t, 2 t + 1
-  float psum[NCG][NS][4];         // 8 sum of P sv, as rounded: columns 2 t and 2 t + 1, twice
+  float psum[NCG][4];             // 8 sum of P sv, as rounded: rows g and g + 8 of a tile whose rows 16 / NS n .. are set n's
   float m[NCG][2], l[NCG][2];     // maximum (in log2 units, as of the last move of the base) and sum
   float mneg[NCG][2];             // -m, or 0 in a column that has seen no key yet (its p are 0)
   float limit[NCG][2];            // a raw score above this moves the base
@@ -434,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
           else x0 = sum;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[cg][grp][0][i] = acc[cg][grp][1][i] = psum[cg][grp / F][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[cg][grp][0][i] = acc[cg][grp][1][i] = psum[cg][i] = 0.f;
       }
       // Row k of this operand is part k / G of group k % G (d = 128: parts 0 and 1 in b0, 2 and 3 in b1;
       // d = 64: 0 to 3 in b0), so that a row of K's scales, repeated, is the other operand.
@@ -467,8 +482,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     for (int i = 0; i < NS; ++i) rinv[i] = pow2(106);
   };
 
-  const int first_len = len;
-  if (mine > 0) read_q(b, h * cols.blocks + cb);
+  if (left > 0) read_q(b, h * cols.blocks + cb);
   int produced = 0;
   for (; produced < R && left > 0; ++produced) produce(produced);
   __syncwarp();
@@ -479,7 +493,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     else return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
   };
 
-  // References that hold the V scales of two tiles (rows of this lane; infinities and NaNs keep theirs):
+  // The set whose sum a lane's row g + 8 r of psum holds.
+  auto set_of_row = [&](int r) { return NS == 4 ? 2 * r + (g >> 2) : NS == 2 ? r : 0; };
+
+  // References that hold the V scales of two tiles (rows of this lane, all finite):
   // 4 times the largest, so that they seldom move.
   auto move_refs = [&](const uint32_t (*vs)[2][G / 2]) {
 #pragma unroll
@@ -487,8 +504,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
       uint32_t x = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t v = vs[i >> 1][i & 1][grp >> 1] >> (16 * (grp & 1)) & 0x7fffu;
-        x = max(x, v < 0x7f80u ? v : 0u);
+        x = max(x, vs[i >> 1][i & 1][grp >> 1] >> (16 * (grp & 1)) & 0x7fffu);
       }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
@@ -501,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (own) psum[cg][grp / F][i] *= down;
+            if (own && set_of_row(i >> 1) == grp / F) psum[cg][i] *= down;
             acc[cg][grp][0][i] *= down;
             acc[cg][grp][1][i] *= down;
           }
@@ -558,7 +574,6 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     }
     const bool edge = bad || k0 + 32 > ulen - a.Sq + 1;
     if (edge) {  // some key is past a column's last one, or its page is missing
-      uint32_t odd = 0;                       // V scales that are not finite, of keys that are there
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
@@ -570,34 +585,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               if (gone || key >= vis[cg][j]) s[tile][cg][2 * r + j] = -INFINITY;
-          // what is not there has no weight and moves no reference; a key that is there, but not for
-          // every column, must not bring its NaN to the others (0 NaN = NaN): out here, in below
 #pragma unroll
-          for (int i = 0; i < G / 2; ++i) {
-            uint32_t& v = vs[tile][r][i];
-            if (gone) v = 0;
-            if ((v & 0x7f80u) == 0x7f80u) odd |= 1u << (tile * 16 + r * 8 + 2 * i), v &= 0xffff0000u;
-            if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (tile * 16 + r * 8 + 2 * i), v &= 0xffffu;
-          }
+          for (int i = 0; i < G / 2; ++i)
+            if (gone) vs[tile][r][i] = 0;  // has no weight and moves no reference
         }
-      if (__any_sync(0xffffffffu, odd != 0)) {
-#pragma unroll
-        for (int cg = 0; cg < NCG; ++cg)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t sees = 0;  // groups in which this column sees one
-            for (int tr = 0; tr < 4; ++tr)
-              if (k0 + tr * 8 + g < vis[cg][j]) sees |= odd >> (tr * 8);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) sees |= __shfl_xor_sync(0xffffffffu, sees, off);
-#pragma unroll
-            for (int grp = 0; grp < G; ++grp)
-              if (sees >> grp & 1) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) acc[cg][grp][i][j] = acc[cg][grp][i][j + 2] = __uint_as_float(0x7fffffffu);
-              }
-          }
-      }
     }
     // The base and the references move seldom: only then are the column's maximum and the largest scales looked for.
     float high[NCG][2];
@@ -610,6 +601,35 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         moves |= high[cg][j] > limit[cg][j];
       }
     if (__any_sync(0xffffffffu, moves)) {
+      // V scales that are not finite leave the products (0 NaN = NaN would reach other groups' sums, and columns
+      // that do not see the key) and go straight to the groups of the columns that see them.
+      uint32_t odd = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int i = 0; i < G / 2; ++i) {
+          uint32_t& v = vs[x >> 1][x & 1][i];
+          if ((v & 0x7f80u) == 0x7f80u) odd |= 1u << (x * 8 + 2 * i), v &= 0xffff0000u;
+          if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (x * 8 + 2 * i), v &= 0xffffu;
+        }
+      if (__any_sync(0xffffffffu, odd != 0)) {
+#pragma unroll
+        for (int cg = 0; cg < NCG; ++cg)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t sees = 0;
+            for (int x = 0; x < 4; ++x)
+              if (k0 + x * 8 + g < vis[cg][j]) sees |= odd >> (x * 8);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) sees |= __shfl_xor_sync(0xffffffffu, sees, off);
+#pragma unroll
+            for (int grp = 0; grp < G; ++grp)
+              if (sees >> grp & 1) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[cg][grp][i][j] = acc[cg][grp][i][j + 2] = __uint_as_float(0x7fffffffu);
+              }
+          }
+      }
       move_refs(vs);
 #pragma unroll
       for (int cg = 0; cg < NCG; ++cg)
@@ -630,8 +650,8 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
                 acc[cg][grp][i][j] *= alpha;
                 acc[cg][grp][i][j + 2] *= alpha;
               }
-#pragma unroll
-            for (int n = 0; n < NS; ++n) psum[cg][n][j] *= alpha;
+            psum[cg][j] *= alpha;
+            psum[cg][j + 2] *= alpha;
             m[cg][j] = v;
             mneg[cg][j] = -v;
             limit[cg][j] = __fdividef(v + kRebase, fac[cg][j]);
@@ -655,13 +675,14 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         const float v_lo = scale_at(vs[tile][0], n) * rinv[n], v_hi = scale_at(vs[tile][1], n) * rinv[n];
-        const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+        const uint32_t e0 = set_of_row(0) == n ? 0x00080008u : 0u, e1 = set_of_row(1) == n ? 0x00080008u : 0u;
+        const uint32_t eights[4] = {e0, e1, e0, e1};
         uint32_t b0[NCG], b1[NCG];
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg) {
           b0[cg] = transposed(pack_f16x2(s[tile][cg][0] * v_lo, s[tile][cg][1] * v_lo));
           b1[cg] = transposed(pack_f16x2(s[tile][cg][2] * v_hi, s[tile][cg][3] * v_hi));
-          mma_f16(psum[cg][n], eights, b0[cg], b1[cg]);
+          mma_f16(psum[cg], eights, b0[cg], b1[cg]);
         }
 #pragma unroll
         for (int grp = n * F; grp < n * F + F; ++grp) {
@@ -693,6 +714,12 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        float eight[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const float x = psum[cg][(NS == 4 ? n >> 1 : n) * 2 + j];
+          eight[n] = NS == 4 ? __shfl_sync(0xffffffffu, x, 16 * (n & 1) + t) : x;
+        }
         if (o_at[cg][j] >= 0) {
           const int c = (cg * 8 + 2 * t + j) & (C::kCols - 1);
           const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
@@ -701,7 +728,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
             // 1 / rinv, exactly; raw numerators are in units of 2^-24 (2^-20: odd channels)
-            const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv, less8 = psum[cg][n][j] * pow2(24);
+            const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv, less8 = eight[n] * pow2(24);
             float y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -722,23 +749,20 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     which = 1;
   };
 
-  if (mine > 0) begin_unit(first_len);  // while the first stages are on their way
   int slot = 0;
   uint32_t phase = 0;
   while (consumed < produced) {
+    const int4 md = meta[slot];
+    const int k0 = md.z & -C::kKeys, flags = md.z & (C::kKeys - 1), ulen = md.w;
+    if (flags & 1) {
+      if (consumed) read_q(md.x, md.y);
+      begin_unit(ulen);
+      seg_k0 = k0;
+    }
     const bool full = mbar_wait(&bars[slot], phase);
     if (!__all_sync(0xffffffffu, full)) {
       ok = false;
       break;
-    }
-    const int4 md = meta[slot];
-    const int k0 = md.z & -C::kKeys, flags = md.z & (C::kKeys - 1), ulen = md.w;
-    if (flags & 1) {
-      if (consumed) {
-        read_q(md.x, md.y);
-        begin_unit(ulen);
-      }
-      seg_k0 = k0;
     }
     const uint8_t* base = ring + slot * C::kStage;
 #pragma unroll 1
@@ -825,8 +849,8 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
       if (ch == 0 && a.lse)
         a.lse[(static_cast<size_t>(first.b) * a.Hq + hq) * a.Sq + sq] = sum == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(sum)) * kLn2;
     } else {
-      // what leaves the CTA: slot 0 for the segment with the run's first stage, slot 1 for the one with its last
-      float* out = my_slots + (W + (i0 == 0 ? 0 : 1)) * C::kSlotFloats;
+      // what leaves the CTA: slot 0 for the unit that its run starts in, slot 1 for one that starts later
+      float* out = my_slots + (W + (first.b == first_unit->x && first.u == first_unit->y ? 0 : 1)) * C::kSlotFloats;
       *reinterpret_cast<float4*>(out + c * D + ch) = O;
       if (ch == 0) *reinterpret_cast<float2*>(out + C::kCols * D + 2 * c) = make_float2(M, sum);
     }
@@ -844,12 +868,12 @@ __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(con
   pdl_wait();  // the first kernel has finished and its slots are visible
   const Run run = runs[i];
   const long long total = runs[ctas].x, before = runs[i - 1].x;
-  // The unit at the boundary starts at stage `first`; the boundary is the unit's first one, or another CTA's.
+  // The first stage of the unit at the boundary; the boundary is the unit's first one, or another CTA's.
   const long long first = run.x - run.st;
   if (run.x >= total || run.st == 0 || first < before) return;
   // It has parts in CTA i - 1 and in every later one that starts inside it.
   const int n = 1 + __syncthreads_count(tid + i < ctas && runs[min(tid + i, ctas)].x < first + run.nst);
-  const int late = before < first ? 1 : 0;
+  const int late = before + 1 < first ? 1 : 0;  // the unit starts after CTA i - 1's run does
   const int heads = a.Hq / a.pages.Hkv, live_cols = heads * a.Sq;
   const int uh = run.u / cols.blocks, c0 = (run.u - uh * cols.blocks) * cols.per;
   const int items = cols.per * (D / 4), rows = kCombineThreads / items;
