@@ -51,24 +51,23 @@ constexpr float kRebase = 8.f;  // move the exponent base only when the maximum 
 
 template <int D, int NCG, int F>
 struct Cfg {
-#ifndef KV4_W1
-#define KV4_W1 12
-#define KV4_W2 8
-#define KV4_T1 4
-#define KV4_T2 4
+#ifndef KV4_WF
+#define KV4_WF 15
+#define KV4_W1 15
+#define KV4_W2 7
 #endif
-  static constexpr int W = NCG == 1 ? KV4_W1 : KV4_W2;  // warps
-  static constexpr int T = NCG == 1 ? KV4_T1 : KV4_T2;  // tiles of a stage
-  static constexpr int kKeys = 16 * T;
+  static constexpr int W = F == 2 ? KV4_WF : NCG == 1 ? KV4_W1 : KV4_W2;  // warps that compute; one more brings the stages
+  static constexpr int kKeys = 32;                      // of a stage: two tiles
+  static constexpr int kThreads = (W + 1) * 32;
   static constexpr int G = D / 32;
   static constexpr int N = G / F;  // groups, or pairs of groups (F = 2), that share a set of MMA columns
   static constexpr int kTile = kv4_tile_bytes(D);
-  static constexpr int kStage = T * kTile;
-  static constexpr int kFit = kRingBudget / (W * (kStage + 24));
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kFit = kRingBudget / (W * (kStage + 32));
   static constexpr int R = kFit < 8 ? kFit : 8;  // stages of a warp's ring
   static constexpr int kOffMeta = W * R * kStage;
   static constexpr int kOffBars = kOffMeta + W * R * 16;
-  static constexpr int kOffSegs = kOffBars + W * R * 8;
+  static constexpr int kOffSegs = kOffBars + 2 * W * R * 8;  // full and free barriers
   static constexpr int kSmem = kOffSegs + 2 * W * 16 + 16;
   static constexpr int kCols = 8 * NCG / F;
   static constexpr int kSlotFloats = kCols * (D + 2);  // numerators [col][D], then (maximum, sum) [col]
@@ -133,6 +132,26 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
+// Contiguous global -> shared copy of `bytes`, completing on `bar`, issued by this thread.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Whether the phase of the given parity has completed; does not wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // G bf16 scales, packed.
 template <int G>
 __device__ __forceinline__ void lds_scales(const uint8_t* p, uint32_t* w) {
@@ -168,34 +187,19 @@ struct Columns {
   int blocks, per;  // column blocks of a KV head's group, columns of each (the last may have fewer)
 };
 
+// The warp that brings the stages: lane i those of warp i's run, into that warp's ring.
 template <int D, int NCG, int F>
-__global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
-    decode_kv4_kernel(const DecodeKv4Args a, const Columns cols, Run* runs, float* slots) {
+__device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Columns& cols, Run* runs, uint8_t* ring, int4* meta, uint64_t* full,
+                                             uint64_t* free_, int2* first_unit) {
   using C = Cfg<D, NCG, F>;
-  constexpr int R = C::R, G = C::G, W = C::W;
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int R = C::R, W = C::W;
   const Kv4Pages& pg = a.pages;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * R * C::kStage;
-  int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + warp * R;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBars) + warp * R;
-  Segment* segs = reinterpret_cast<Segment*>(smem + C::kOffSegs);
-  int2* first_unit = reinterpret_cast<int2*>(segs + 2 * W);  // the unit that the CTA's run starts in
+  const int lane = threadIdx.x & 31;
   const int units = pg.Hkv * cols.blocks;
-  const int heads = a.Hq / pg.Hkv, live_cols = heads * a.Sq;
   const int tiles_shift = pg.page_shift - 4;
-  float* const my_slots = slots + static_cast<size_t>(blockIdx.x) * C::kSlots * C::kSlotFloats;
+  const long long page_bytes = (static_cast<long long>(pg.Hkv) << tiles_shift) * C::kTile;
 
-  if (lane == 0) {
-    for (int r = 0; r < R; ++r) mbar_init(&bars[r], 1);
-    fence_mbar_init();
-  }
-  if (lane < 2) segs[2 * warp + lane].b = -1;
-  pdl_launch_dependents();
-  __syncwarp();
-
-  // The stages of the call, cut for the CTAs and then for the warps of each.
+  // All units' costs, cut for the CTAs and then for the warps of each.
   const int len0 = lane < pg.B ? checked_len(pg, lane) : 0;  // of the first 32 sequences
   long long total = cost_of<C::kKeys>(len0);
   for (int b = lane + 32; b < pg.B; b += 32) total += cost_of<C::kKeys>(checked_len(pg, b));
@@ -209,153 +213,202 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   const long long n_cta = each + (cta < more);
   const long long each_w = n_cta >> 32 ? n_cta / W : static_cast<unsigned>(n_cta) / W;
   const unsigned more_w = static_cast<unsigned>(n_cta - each_w * W);
-  const long long x0 = cta_x + each_w * warp + min(static_cast<unsigned>(warp), more_w);
-  int left = static_cast<int>(each_w + (warp < more_w));  // stages still to be produced
-  const bool any = left > 0;
+  const long long x0 = cta_x + each_w * lane + min(static_cast<unsigned>(lane), more_w);
+  int left = lane < W ? static_cast<int>(each_w + (lane < more_w)) : 0;  // stages still to be brought
 
-  // The producer's place: stage st (of nst) of column block cb of KV head h of sequence b.
+  // The place: stage st (of nst) of column block cb of KV head h of sequence b.
   int b = 0, h = 0, cb = 0, st = 0, nst = 0, len = 0;
-  if (any) {
-    long long base = 0;  // costs of a KV head's units before this group of 32 sequences
-    for (int c = 0; c < pg.B; c += 32) {
-      const int l = c == 0 ? len0 : c + lane < pg.B ? checked_len(pg, c + lane) : 0;
-      const int n = cost_of<C::kKeys>(l);
-      long long pre = n;
+  bool placed = left == 0;
+  long long base = 0;  // costs of a KV head's units before this group of 32 sequences
+  for (int c = 0; c < pg.B && !__all_sync(0xffffffffu, placed); c += 32) {
+    const int l = c == 0 ? len0 : c + lane < pg.B ? checked_len(pg, c + lane) : 0;
+    long long pre = cost_of<C::kKeys>(l);
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, pre, off);
-        if (lane >= off) pre += v;
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, pre, off);
+      if (lane >= off) pre += v;
+    }
+    pre += base;
+    int lo = 0;  // sequences of the group that end at or before x0
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1) {
+      const long long v = __shfl_sync(0xffffffffu, pre, lo + step - 1);
+      if (v * units <= x0) lo += step;
+    }
+    base = __shfl_sync(0xffffffffu, pre, 31);
+    const int ll = __shfl_sync(0xffffffffu, l, lo);
+    const long long end = __shfl_sync(0xffffffffu, pre, lo);
+    if (!placed && end * units > x0) {
+      placed = true;
+      b = c + lo;
+      len = ll;
+      const int cost = cost_of<C::kKeys>(ll);
+      const long long in = x0 - (end - cost) * units;
+      const int u = static_cast<int>(in >> 32 ? in / cost : static_cast<unsigned>(in) / static_cast<unsigned>(cost));
+      nst = cost - 1;
+      st = static_cast<int>(in - static_cast<long long>(u) * cost) - 1;
+      if (st < 0) {  // the unit's start, which is no stage
+        st = 0;
+        --left;
       }
-      pre += base;
-      const unsigned past = __ballot_sync(0xffffffffu, pre * units > x0);
-      if (past) {
-        const int src = __ffs(past) - 1;
-        b = c + src;
-        len = __shfl_sync(0xffffffffu, l, src);
-        const int cost = __shfl_sync(0xffffffffu, n, src);
-        const long long in = x0 - (__shfl_sync(0xffffffffu, pre, src) - cost) * units;
-        const int u = static_cast<int>(in >> 32 ? in / cost : static_cast<unsigned>(in) / static_cast<unsigned>(cost));
-        nst = cost - 1;
-        st = static_cast<int>(in - static_cast<long long>(u) * cost) - 1;
-        if (st < 0) {  // the unit's start, which is no stage
-          st = 0;
-          --left;
-        }
-        h = u / cols.blocks;
-        cb = u - h * cols.blocks;
-        break;
-      }
-      base = __shfl_sync(0xffffffffu, pre, 31);
+      h = u / cols.blocks;
+      cb = u - h * cols.blocks;
     }
   }
-  if (warp == 0 && lane == 0) {
+  if (lane == 0) {
     runs[cta] = Run{cta_x, b, h * cols.blocks + cb, st, nst, 0};
     if (cta + 1 == ctas) runs[ctas].x = total;
     *first_unit = make_int2(b, h * cols.blocks + cb);
   }
-  if (warp == W - 1) {  // sequences without a token are shared out among the CTAs
-    for (int b0 = cta; b0 < pg.B; b0 += 32 * ctas) {
-      const int bl = b0 + lane * ctas;
-      unsigned none = __ballot_sync(0xffffffffu, bl < pg.B && checked_len(pg, bl) == 0);
-      for (; none; none &= none - 1) {
-        const size_t be = b0 + (__ffs(none) - 1) * ctas;
-        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + be * a.Sq * a.Hq * D);
-        for (int i = lane; i < a.Sq * a.Hq * (D / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.lse)
-          for (int i = lane; i < a.Sq * a.Hq; i += 32) a.lse[be * a.Sq * a.Hq + i] = -INFINITY;
-      }
-    }
+  if (lane < W && left == 0) {  // an empty run
+    meta[0] = make_int4(-1, 0, 0, 0);
+    mbar_arrive(&full[0]);
   }
 
-  int consumed = 0;
-  bool fresh = true;           // the next stage is its run's first of a unit
-  int win = 0, ids = 0;        // lane i holds the page id of page win + i of sequence b
-  int win_end = 0;             // 0: no such window yet
-  int in_page = 0;             // stages left in the page at src
-  const uint8_t* src = nullptr;
-  const long long page_bytes = static_cast<long long>(pg.Hkv << tiles_shift) * C::kTile;
-  auto page_of = [&](int p) -> int {
-    if (p >= win_end) {
-      win = p;
-      win_end = p + 32;
-      ids = 0;
-      if ((static_cast<long long>(p + lane) << pg.page_shift) < len) {
-        ids = pg.table[static_cast<size_t>(b) * pg.max_pages + p + lane];
-        if (static_cast<unsigned>(ids) >= static_cast<unsigned>(pg.n_pages)) {
-          atomicCAS(pg.err, 0, kErrDeviceArg);
-          ids = -1;
-        }
-      }
-    }
-    return __shfl_sync(0xffffffffu, ids, p - win);
+  // The page id of page p of sequence b; -1 where there is no such page of the pool, 0 (of no use) past the sequence's end.
+  auto page_id = [&](int p) -> int {
+    if (static_cast<long long>(p) << pg.page_shift >= len) return 0;
+    const int id = pg.table[static_cast<size_t>(b) * pg.max_pages + p];
+    return static_cast<unsigned>(id) < static_cast<unsigned>(pg.n_pages) ? id : -1;
   };
-  int missing = 0;  // the page at src does not exist
-  auto produce = [&](int slot) {
-    if (st == nst) {  // the next unit, in the next sequence that has one
-      st = 0;
-      fresh = true;
-      win_end = 0;
-      in_page = 0;
-      if (++cb == cols.blocks) {
-        cb = 0;
-        if (++h == pg.Hkv) {
-          h = 0;
-          do {
-            ++b;
-            len = b < pg.B ? checked_len(pg, b) : 1;  // past the end only where lengths changed under the call
-          } while (len == 0);
-          b = min(b, pg.B - 1);
-          nst = (len + C::kKeys - 1) / C::kKeys;
-        }
+  // Ids are read ahead: of the page (for pages of one tile, of both tiles) of the next stage, and of the page after.
+  int id = 0, id_next = 0, id_first = 0;
+  auto look = [&]() {
+    const int p = (st * C::kKeys) >> pg.page_shift;
+    id = page_id(p);
+    id_next = page_id(p + 1);
+  };
+  if (left > 0) {
+    look();
+    id_first = st == 0 ? id : page_id(0);
+  }
+  bool fresh = true;  // the next stage is its run's first of a unit
+  int issued = 0, slot = 0;
+  uint32_t phase = 1;  // parity of the slot's last release; the first round finds every slot free
+  uint64_t since = globaltimer_ns();
+  while (__any_sync(0xffffffffu, left > 0)) {
+    const bool go = left > 0 && mbar_test(&free_[slot], phase);
+    if (go) {
+      const int k0 = st * C::kKeys, ntiles = len - k0 > 16 ? 2 : 1;
+      uint8_t* dst = ring + slot * C::kStage;
+      const uint8_t *src0 = nullptr, *src1 = nullptr;
+      uint32_t bytes0 = ntiles * C::kTile;
+      int bad;
+      if (tiles_shift > 0) {
+        bad = id < 0 ? 3 : 0;
+        if (id >= 0) src0 = pg.pool + id * page_bytes + ((static_cast<long long>(h) << tiles_shift) + ((k0 >> 4) & ((1 << tiles_shift) - 1))) * C::kTile;
+      } else {  // pages of one tile
+        bad = (id < 0 ? 1 : 0) | (id_next < 0 && ntiles == 2 ? 2 : 0);
+        bytes0 = C::kTile;
+        if (id >= 0) src0 = pg.pool + id * page_bytes + static_cast<long long>(h) * C::kTile;
+        if (id_next >= 0 && ntiles == 2) src1 = pg.pool + id_next * page_bytes + static_cast<long long>(h) * C::kTile;
       }
-    }
-    const int k0 = st * C::kKeys;
-    const int ntiles = min((len - k0 + 15) >> 4, C::T);
-    uint8_t* dst = ring + slot * C::kStage;
-    uint64_t* bar = &bars[slot];
-    int bad = 0;
-    if (1 << tiles_shift >= C::T) {
-      if (in_page == 0) {
-        const int p = page_of(k0 >> pg.page_shift);
-        const int at = (k0 >> 4) & ((1 << tiles_shift) - 1);
-        missing = p < 0 ? (1 << C::T) - 1 : 0;
-        src = pg.pool + max(p, 0) * page_bytes + ((static_cast<long long>(h) << tiles_shift) + at) * C::kTile;
-        in_page = ((1 << tiles_shift) - at) / C::T;
+      if (bad) atomicCAS(pg.err, 0, kErrDeviceArg);
+      const int this_b = b, this_u = h * cols.blocks + cb, this_len = len;
+      int flags = (fresh ? 1 : 0) | bad << 2;
+      fresh = false;
+      --left;
+      ++st;
+      if (st == nst && left > 0) --left;  // the next unit's start
+      if (st == nst || left == 0) flags |= 2;
+      meta[slot] = make_int4(this_b, this_u, k0 | flags, left == 0 ? this_len | static_cast<int>(0x80000000u) : this_len);
+      mbar_arrive_expect_tx(&full[slot], (src0 ? bytes0 : 0u) + (src1 ? C::kTile : 0u));
+      if (src0) bulk_load(dst, src0, bytes0, &full[slot]);
+      if (src1) bulk_load(dst + C::kTile, src1, C::kTile, &full[slot]);
+      ++issued;
+      if (++slot == R) {
+        slot = 0;
+        phase ^= 1;
       }
-      bad = missing;
-      const uint32_t bytes = bad ? 0 : ntiles * C::kTile;
-      mbar_arrive_expect_tx_elect(bar, bytes);
-      if (bytes) bulk_load_elect(dst, src, bytes, bar);
-      src += C::kStage;
-      --in_page;
-    } else {  // a stage of several pages
-      const uint8_t* at[C::T];
-      uint32_t bytes = 0;
-#pragma unroll
-      for (int i = 0; i < C::T; ++i) {
-        at[i] = nullptr;
-        if (i < ntiles && (i & ((1 << tiles_shift) - 1)) == 0) {
-          const int p = page_of((k0 >> pg.page_shift) + (i >> tiles_shift)), nt = min(1 << tiles_shift, ntiles - i);
-          if (p < 0) {
-            bad |= ((1 << nt) - 1) << i;
-          } else {
-            at[i] = pg.pool + p * page_bytes + (static_cast<long long>(h) << tiles_shift) * C::kTile;
-            bytes += nt * C::kTile;
+      if (left > 0) {
+        if (st == nst) {  // the next unit, in the next sequence that has one
+          st = 0;
+          fresh = true;
+          bool moved = false;
+          if (++cb == cols.blocks) {
+            cb = 0;
+            if (++h == pg.Hkv) {
+              h = 0;
+              moved = true;
+              do {
+                ++b;
+                len = b < pg.B ? checked_len(pg, b) : 1;  // past the end only where lengths changed under the call
+              } while (len == 0);
+              b = min(b, pg.B - 1);
+              nst = (len + C::kKeys - 1) / C::kKeys;
+            }
           }
+          if (moved) id_first = page_id(0);
+          id = id_first;
+          id_next = page_id(1);
+        } else if (tiles_shift == 0) {
+          look();
+        } else if (((st * C::kKeys) & ((1 << pg.page_shift) - 1)) == 0) {
+          id = id_next;
+          id_next = page_id(((st * C::kKeys) >> pg.page_shift) + 1);
         }
       }
-      mbar_arrive_expect_tx_elect(bar, bytes);
-#pragma unroll
-      for (int i = 0; i < C::T; ++i)
-        if (at[i]) bulk_load_elect(dst + i * C::kTile, at[i], min(1 << tiles_shift, ntiles - i) * C::kTile, bar);
     }
-    --left;
-    ++st;
-    const int flags = (fresh ? 1 : 0) | (st == nst || left == 0 ? 2 : 0) | bad << 2;
-    if (st == nst && left > 0) --left;  // the next unit's start
-    fresh = false;
-    if (lane == 0) meta[slot] = make_int4(b, h * cols.blocks + cb, k0 | flags, len);
-  };
+    if (__any_sync(0xffffffffu, go)) {
+      since = globaltimer_ns();
+    } else {
+      if (globaltimer_ns() - since > kWaitLimitNs) {
+        if (lane == 0) atomicCAS(pg.err, 0, kErrDeviceTimeout);
+        break;
+      }
+      __nanosleep(100);
+    }
+  }
+  // Every copy lands before the CTA retires.
+  for (int i = max(issued - R, 0); i < issued; ++i) mbar_wait(&full[i % R], (i / R) & 1);
+  __syncwarp();
+}
+
+template <int D, int NCG, int F>
+__global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
+    decode_kv4_kernel(const DecodeKv4Args a, const Columns cols, Run* runs, float* slots) {
+  using C = Cfg<D, NCG, F>;
+  constexpr int R = C::R, G = C::G, W = C::W;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Kv4Pages& pg = a.pages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  Segment* segs = reinterpret_cast<Segment*>(smem + C::kOffSegs);
+  int2* first_unit = reinterpret_cast<int2*>(segs + 2 * W);  // the unit that the CTA's run starts in
+  const int heads = a.Hq / pg.Hkv, live_cols = heads * a.Sq;
+  float* const my_slots = slots + static_cast<size_t>(blockIdx.x) * C::kSlots * C::kSlotFloats;
+  // Warp w's ring: stages, what they are (sequence, unit, first key | flags, length | last of the run), barriers.
+  const int stream = warp < W ? warp : min(lane, W - 1);
+  uint8_t* ring = smem + stream * R * C::kStage;
+  int4* meta = reinterpret_cast<int4*>(smem + C::kOffMeta) + stream * R;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBars) + stream * R;
+  uint64_t* free_ = full + W * R;
+
+  if (warp == W && lane < W) {
+    for (int r = 0; r < R; ++r) mbar_init(&full[r], 1), mbar_init(&free_[r], 1);
+    fence_mbar_init();
+    segs[2 * lane].b = segs[2 * lane + 1].b = -1;
+  }
+  pdl_launch_dependents();
+  __syncthreads();
+
+  if (warp == W) {
+    bring_stages<D, NCG, F>(a, cols, runs, ring, meta, full, free_, first_unit);
+  } else {
+    if (warp == W - 1) {  // sequences without a token are shared out among the CTAs
+      const int ctas = gridDim.x;
+      for (int b0 = blockIdx.x; b0 < pg.B; b0 += 32 * ctas) {
+        const int bl = b0 + lane * ctas;
+        unsigned none = __ballot_sync(0xffffffffu, bl < pg.B && checked_len(pg, bl) == 0);
+        for (; none; none &= none - 1) {
+          const size_t be = b0 + (__ffs(none) - 1) * ctas;
+          uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + be * a.Sq * a.Hq * D);
+          for (int i = lane; i < a.Sq * a.Hq * (D / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (a.lse)
+            for (int i = lane; i < a.Sq * a.Hq; i += 32) a.lse[be * a.Sq * a.Hq + i] = -INFINITY;
+        }
+      }
+    }
 
   // Columns.  An MMA has 8; with F = 2 the upper four repeat the lower four for the odd groups (of a pair
   // of groups), so that one accumulator holds both groups' sums and a lane scales only its own group's.  This lane:
@@ -363,54 +416,39 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   constexpr int NS = C::N;
   const int half_q = F == 2 ? g >> 2 : 0, half = F == 2 ? t >> 1 : 0;
   const uint32_t pick = half ? 0x3244u : 0x1044u;  // F = 2: this lane's scale of a packed pair, as fp32
-  int at_cb = -1;                 // the column block they are for
-  int q_at[NCG], o_at[NCG][2];    // (token Hq + head in the group); -1: no such column
-  int tok[NCG][2];                // the column's token
   uint32_t qf[NCG][G][4];         // B fragments of q: two MMAs a group
   uint32_t less[NCG][2];          // B fragment of -8 sum of q over each group, in four bf16 parts
   float fac[NCG][2];              // a raw score times this is the score in log2 units
   int vis[NCG][2];                // keys that the column sees
   float acc[NCG][G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and + 1: 16 times as large), columns 2 t, 2 t + 1
   float psum[NCG][4];             // 8 sum of P sv, as rounded: rows g and g + 8 of a tile whose rows 16 / NS n .. are set n's
-  float m[NCG][2], l[NCG][2];     // maximum (in log2 units, as of the last move of the base) and sum
-  float mneg[NCG][2];             // -m, or 0 in a column that has seen no key yet (its p are 0)
-  float limit[NCG][2];            // a raw score above this moves the base
+  float l[NCG][2];                // sum
+  float mneg[NCG][2];             // less the base (the maximum in log2 units when it last moved), or 0 where no key was seen yet
+  float limit[NCG][2];            // a raw score above this moves the base; -inf: no key was seen yet
   float rinv[NS];                 // P sv goes in times this: 2^6 over the reference of the lane's group
   uint32_t ref[G / 2];            // the references as bf16, packed like the scales
   uint32_t my_ref;                // ref[t % (G / 2)]: the lane checks that word of one row in four lanes' turn
   int seg_k0 = 0, which = 0;
-  bool ok = true;
 
-  uint4 raw[NCG][G];              // q as read
-  auto read_q = [&](int ub, int uu) {
-    const int uh = cols.blocks == 1 ? uu : uu / cols.blocks, ucb = uu - uh * cols.blocks;
-    if (ucb != at_cb) {
-      at_cb = ucb;
-#pragma unroll
-      for (int cg = 0; cg < NCG; ++cg)
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const int c = (cg * 8 + (j < 2 ? 2 * t + j : g)) & (C::kCols - 1), col = ucb * cols.per + c;
-          const int hd = a.Sq == 1 ? col : col / a.Sq, tk = col - hd * a.Sq;
-          const int at = c < cols.per && col < live_cols ? tk * a.Hq + hd : -1;
-          if (j < 2) {
-            o_at[cg][j] = at;
-            tok[cg][j] = tk;
-          } else {
-            q_at[cg] = at;
-          }
-        }
-    }
+  // The token and the query head (of the KV head's group) of a column; false where there is none.
+  auto column = [&](int cg, int pc, int c0, int* hd, int* tk) {
+    const int c = (cg * 8 + pc) & (C::kCols - 1), col = c0 + c;
+    *hd = a.Sq == 1 ? col : col / a.Sq;
+    *tk = col - *hd * a.Sq;
+    return c < cols.per && col < live_cols;
+  };
+  auto begin_unit = [&](int ub, int uu, int ulen) {
+    const int uh = cols.blocks == 1 ? uu : uu / cols.blocks, c0 = (uu - uh * cols.blocks) * cols.per;
     const size_t row0 = static_cast<size_t>(ub) * a.Sq * a.Hq + uh * heads;
+    uint4 raw[NCG][G];
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg) {
-      const bool live = q_at[cg] >= 0;
-      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) + (row0 + (live ? q_at[cg] : 0)) * D + 8 * t;
+      int hd, tk;
+      const bool live = column(cg, g, c0, &hd, &tk);
+      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) + (row0 + (live ? tk * a.Hq + hd : 0)) * D + 8 * t;
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) raw[cg][grp] = live ? *reinterpret_cast<const uint4*>(row + 32 * grp) : make_uint4(0u, 0u, 0u, 0u);
     }
-  };
-  auto begin_unit = [&](int ulen) {
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg) {
       uint32_t mx = 0;
@@ -470,8 +508,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         fac[cg][j] = __shfl_sync(0xffffffffu, fc, (2 * t + j) * 4);
-        vis[cg][j] = ulen - a.Sq + 1 + tok[cg][j];
-        m[cg][j] = limit[cg][j] = -INFINITY;
+        int hd, tk;
+        column(cg, 2 * t + j, c0, &hd, &tk);
+        vis[cg][j] = ulen - a.Sq + 1 + tk;
+        limit[cg][j] = -INFINITY;
         mneg[cg][j] = l[cg][j] = 0.f;
       }
     }
@@ -481,11 +521,6 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
 #pragma unroll
     for (int i = 0; i < NS; ++i) rinv[i] = pow2(106);
   };
-
-  if (left > 0) read_q(b, h * cols.blocks + cb);
-  int produced = 0;
-  for (; produced < R && left > 0; ++produced) produce(produced);
-  __syncwarp();
 
   // This lane's scale of set n (its group, or the lane's one of its pair) among packed scales.
   auto scale_at = [&](const uint32_t* w, int n) -> float {
@@ -640,8 +675,9 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
           v *= fac[cg][j];
-          if (v > m[cg][j] + kRebase) {
-            const float alpha = wm_ex2(m[cg][j] - v);
+          const float base2 = limit[cg][j] == -INFINITY ? -INFINITY : -mneg[cg][j];
+          if (v > base2 + kRebase) {
+            const float alpha = wm_ex2(base2 - v);
             l[cg][j] *= alpha;
 #pragma unroll
             for (int grp = 0; grp < G; ++grp)
@@ -652,7 +688,6 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
               }
             psum[cg][j] *= alpha;
             psum[cg][j + 2] *= alpha;
-            m[cg][j] = v;
             mneg[cg][j] = -v;
             limit[cg][j] = __fdividef(v + kRebase, fac[cg][j]);
           }
@@ -699,12 +734,11 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
     }
   };
 
-  auto end_unit = [&](int ub, int uu, bool starts, bool ends) {
-    const int uh = cols.blocks == 1 ? uu : uu / cols.blocks;
+  // The run's last segment goes to the ring, which is free by then.
+  auto end_unit = [&](int ub, int uu, bool starts, bool ends, bool near) {
+    const int uh = cols.blocks == 1 ? uu : uu / cols.blocks, c0 = (uu - uh * cols.blocks) * cols.per;
     const size_t row0 = static_cast<size_t>(ub) * a.Sq * a.Hq + uh * heads;
     const bool whole = starts && ends;
-    // The run's last segment goes to the ring, which is free by then.
-    const bool near = consumed == produced;
     float* slot = near ? reinterpret_cast<float*>(ring) : my_slots + warp * C::kSlotFloats;
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg)
@@ -720,10 +754,12 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
           const float x = psum[cg][(NS == 4 ? n >> 1 : n) * 2 + j];
           eight[n] = NS == 4 ? __shfl_sync(0xffffffffu, x, 16 * (n & 1) + t) : x;
         }
-        if (o_at[cg][j] >= 0) {
+        int hd, tk;
+        if (column(cg, 2 * t + j, c0, &hd, &tk)) {
           const int c = (cg * 8 + 2 * t + j) & (C::kCols - 1);
+          const float base2 = limit[cg][j] == -INFINITY ? -INFINITY : -mneg[cg][j];
           const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (row0 + o_at[cg][j]) * D + 4 * g + 32 * half;
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (row0 + static_cast<size_t>(tk) * a.Hq + hd) * D + 4 * g + 32 * half;
           float* part = slot + c * D + 4 * g + 32 * half;
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
@@ -739,50 +775,42 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
             else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);
           }
           if (g == 0 && half == 0) {
-            if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(m[cg][j], sum);
-            else if (a.lse) a.lse[static_cast<size_t>(ub) * a.Sq * a.Hq + (uh * heads + o_at[cg][j] - tok[cg][j] * a.Hq) * a.Sq + tok[cg][j]] =
-                sum == 0.f ? -INFINITY : (m[cg][j] + log2f(sum)) * kLn2;
+            if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(base2, sum);
+            else if (a.lse) a.lse[(static_cast<size_t>(ub) * a.Hq + uh * heads + hd) * a.Sq + tk] = sum == 0.f ? -INFINITY : (base2 + log2f(sum)) * kLn2;
           }
         }
       }
+    __syncwarp();
     if (!whole && lane == 0) segs[2 * warp + which] = Segment{ub, uu, starts | ends << 1, near};
     which = 1;
   };
 
   int slot = 0;
   uint32_t phase = 0;
-  while (consumed < produced) {
-    const int4 md = meta[slot];
-    const int k0 = md.z & -C::kKeys, flags = md.z & (C::kKeys - 1), ulen = md.w;
-    if (flags & 1) {
-      if (consumed) read_q(md.x, md.y);
-      begin_unit(ulen);
-      seg_k0 = k0;
-    }
-    const bool full = mbar_wait(&bars[slot], phase);
-    if (!__all_sync(0xffffffffu, full)) {
-      ok = false;
+  while (true) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) {
+      if (lane == 0) atomicCAS(pg.err, 0, kErrDeviceTimeout);
       break;
     }
-    const uint8_t* base = ring + slot * C::kStage;
-#pragma unroll 1
-    for (int i = 0; i < C::T && k0 + 16 * i < ulen; i += 2) two_tiles(base + i * C::kTile, k0 + 16 * i, flags >> (2 + i) & 3, ulen);
-    __syncwarp();
-    ++consumed;
-    if (left > 0) {
-      produce(slot);
-      ++produced;
+    const int4 md = meta[slot];
+    if (md.x < 0) break;  // an empty run
+    const int k0 = md.z & ~31, flags = md.z & 31, ulen = md.w & 0x7fffffff;
+    if (flags & 1) {
+      begin_unit(md.x, md.y, ulen);
+      seg_k0 = k0;
     }
+    two_tiles(ring + slot * C::kStage, k0, flags >> 2, ulen);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&free_[slot]);
     if (++slot == R) {
       slot = 0;
       phase ^= 1;
     }
-    if (flags & 2) end_unit(md.x, md.y, seg_k0 == 0, k0 + C::kKeys >= ulen);
+    if (flags & 2) {
+      end_unit(md.x, md.y, seg_k0 == 0, k0 + C::kKeys >= ulen, md.w < 0);
+      if (md.w < 0) break;
+    }
   }
-  if (!ok) {
-    if (lane == 0) atomicCAS(pg.err, 0, kErrDeviceTimeout);
-    // every copy that this warp started lands before the CTA retires
-    for (int c = consumed; c < produced; ++c) mbar_wait(&bars[c % R], (c / R) & 1);
   }
   __syncthreads();
 
@@ -796,7 +824,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::W * 32, 1)
   const unsigned endings = __ballot_sync(0xffffffffu, sg.b >= 0 && (sg.ends & 2));
   const int items = cols.per * (D / 4);
   int i0 = __ffs(firsts) - 1, passed = 0;  // the first segment of the unit at hand; units before it, times items
-  for (int at = threadIdx.x; firsts; at += W * 32) {
+  for (int at = threadIdx.x; firsts; at += C::kThreads) {
     while (i0 >= 0 && at >= passed + items) {
       passed += items;
       i0 = __ffs(firsts & ~((2u << i0) - 1u)) - 1;
@@ -957,7 +985,7 @@ cudaError_t launch_dn(const Columns cols, const DecodeKv4Args& a, cudaStream_t s
   const int grid = most < sms ? most : sms;
   Run* runs = static_cast<Run*>(a.work);
   float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(a.work) + kRunsBytes);
-  decode_kv4_kernel<D, NCG, F><<<grid, C::W * 32, C::kSmem, s>>>(a, cols, runs, slots);
+  decode_kv4_kernel<D, NCG, F><<<grid, C::kThreads, C::kSmem, s>>>(a, cols, runs, slots);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid == 1) return e;
   return launch_after_pdl(decode_kv4_combine_kernel<D, NCG, F>, dim3(grid - 1), dim3(kCombineThreads), 0, s, a, cols, grid,
