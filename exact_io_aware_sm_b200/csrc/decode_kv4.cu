@@ -47,7 +47,7 @@ constexpr int kMaxCtas = 148;
 constexpr int kRingBudget = 222 * 1024;
 constexpr int kCombineThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kRebase = 8.f;  // move the exponent base only when the maximum grows by more
+constexpr float kMostWeight = 256.f;  // of a lane's four keys of a column, relative to the base: more moves the base
 
 template <int D, int NCG, int F>
 struct Cfg {
@@ -173,6 +173,16 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Bytes 1 and 3 of a word as 16-bit numbers.
+__device__ __forceinline__ uint32_t high_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
+
+// Differences of two fp16 pairs (of subnormal numbers: exact).
+__device__ __forceinline__ uint32_t less_f16x2(uint32_t x, uint32_t y) {
+  uint32_t z;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+  return z;
 }
 
 // Products of two bf16 pairs.
@@ -423,8 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
   float acc[NCG][G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and + 1: 16 times as large), columns 2 t, 2 t + 1
   float psum[NCG][4];             // 8 sum of P sv, as rounded: rows g and g + 8 of a tile whose rows 16 / NS n .. are set n's
   float l[NCG][2];                // sum
-  float mneg[NCG][2];             // less the base (the maximum in log2 units when it last moved), or 0 where no key was seen yet
-  float limit[NCG][2];            // a raw score above this moves the base; -inf: no key was seen yet
+  float mneg[NCG][2];             // less the base (the maximum in log2 units when it last moved); inf: no key was seen yet
   float rinv[NS];                 // P sv goes in times this: 2^6 over the reference of the lane's group
   uint32_t ref[G / 2];            // the references as bf16, packed like the scales
   uint32_t my_ref;                // ref[t % (G / 2)]: the lane checks that word of one row in four lanes' turn
@@ -511,8 +520,8 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
         int hd, tk;
         column(cg, 2 * t + j, c0, &hd, &tk);
         vis[cg][j] = ulen - a.Sq + 1 + tk;
-        limit[cg][j] = -INFINITY;
-        mneg[cg][j] = l[cg][j] = 0.f;
+        mneg[cg][j] = INFINITY;
+        l[cg][j] = 0.f;
       }
     }
 #pragma unroll
@@ -588,8 +597,8 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) {
         const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[1][grp] & 0x000f000fu, w[0][grp] & 0x00f000f0u, w[1][grp] & 0x00f000f0u};
-        const uint32_t v0 = w[0][grp] >> 8, v1 = w[1][grp] >> 8;
-        const uint32_t f1[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u};
+        const uint32_t v0 = high_bytes(w[0][grp]), v1 = high_bytes(w[1][grp]), l0 = v0 & 0x000f000fu, l1 = v1 & 0x000f000fu;
+        const uint32_t f1[4] = {l0, l1, less_f16x2(v0, l0), less_f16x2(v1, l1)};
         const float k_lo = scale_at(ks[0], grp / F), k_hi = scale_at(ks[1], grp / F);
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg) {
@@ -625,16 +634,23 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
             if (gone) vs[tile][r][i] = 0;  // has no weight and moves no reference
         }
     }
-    // The base and the references move seldom: only then are the column's maximum and the largest scales looked for.
-    float high[NCG][2];
+    // The base and the references move seldom, where weights or scales have grown too large for them: only then are
+    // the column's maximum and the largest scales looked for.
+    float p[2][NCG][4], some[NCG][2];
+    auto weights = [&](int cg, float n0, float n1) {
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[tile][cg][i] = wm_ex2(fmaf(s[tile][cg][i], fac[cg][i & 1], i & 1 ? n1 : n0));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) some[cg][j] = (p[0][cg][j] + p[0][cg][j + 2]) + (p[1][cg][j] + p[1][cg][j + 2]);
+    };
     bool moves = edge || __vmaxu2(__vmaxu2(check[0], check[1]), my_ref) != my_ref;
 #pragma unroll
-    for (int cg = 0; cg < NCG; ++cg)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        high[cg][j] = fmaxf(fmaxf(s[0][cg][j], s[0][cg][j + 2]), fmaxf(s[1][cg][j], s[1][cg][j + 2]));
-        moves |= high[cg][j] > limit[cg][j];
-      }
+    for (int cg = 0; cg < NCG; ++cg) {
+      weights(cg, mneg[cg][0], mneg[cg][1]);
+      moves |= some[cg][0] > kMostWeight || some[cg][1] > kMostWeight;
+    }
     if (__any_sync(0xffffffffu, moves)) {
       // V scales that are not finite leave the products (0 NaN = NaN would reach other groups' sums, and columns
       // that do not see the key) and go straight to the groups of the columns that see them.
@@ -667,17 +683,16 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
       }
       move_refs(vs);
 #pragma unroll
-      for (int cg = 0; cg < NCG; ++cg)
+      for (int cg = 0; cg < NCG; ++cg) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float v = high[cg][j];
+          float v = fmaxf(fmaxf(s[0][cg][j], s[0][cg][j + 2]), fmaxf(s[1][cg][j], s[1][cg][j + 2]));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
           v *= fac[cg][j];
-          const float base2 = limit[cg][j] == -INFINITY ? -INFINITY : -mneg[cg][j];
-          if (v > base2 + kRebase) {
-            const float alpha = wm_ex2(base2 - v);
+          if (v > -mneg[cg][j]) {
+            const float alpha = wm_ex2(-mneg[cg][j] - v);
             l[cg][j] *= alpha;
 #pragma unroll
             for (int grp = 0; grp < G; ++grp)
@@ -689,24 +704,22 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
             psum[cg][j] *= alpha;
             psum[cg][j + 2] *= alpha;
             mneg[cg][j] = -v;
-            limit[cg][j] = __fdividef(v + kRebase, fac[cg][j]);
           }
         }
+        // a column that still sees no key has weights 0
+        weights(cg, mneg[cg][0] == INFINITY ? 0.f : mneg[cg][0], mneg[cg][1] == INFINITY ? 0.f : mneg[cg][1]);
+      }
     }
 #pragma unroll
+    for (int cg = 0; cg < NCG; ++cg)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) l[cg][j] += some[cg][j];
+#pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
-      const uint8_t* p = base + tile * C::kTile;
+      const uint8_t* at = base + tile * C::kTile;
       uint32_t w[2][G];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) lds_words<G>(p + kv4_off_v(D) + ((r * 8 + g) * 4 + t) * (4 * G), w[r]);
-#pragma unroll
-      for (int cg = 0; cg < NCG; ++cg)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float& x = s[tile][cg][i];
-          x = wm_ex2(fmaf(x, fac[cg][i & 1], mneg[cg][i & 1]));
-          l[cg][i & 1] += x;
-        }
+      for (int r = 0; r < 2; ++r) lds_words<G>(at + kv4_off_v(D) + ((r * 8 + g) * 4 + t) * (4 * G), w[r]);
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         const float v_lo = scale_at(vs[tile][0], n) * rinv[n], v_hi = scale_at(vs[tile][1], n) * rinv[n];
@@ -715,15 +728,16 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
         uint32_t b0[NCG], b1[NCG];
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg) {
-          b0[cg] = transposed(pack_f16x2(s[tile][cg][0] * v_lo, s[tile][cg][1] * v_lo));
-          b1[cg] = transposed(pack_f16x2(s[tile][cg][2] * v_hi, s[tile][cg][3] * v_hi));
+          b0[cg] = transposed(pack_f16x2(p[tile][cg][0] * v_lo, p[tile][cg][1] * v_lo));
+          b1[cg] = transposed(pack_f16x2(p[tile][cg][2] * v_hi, p[tile][cg][3] * v_hi));
           mma_f16(psum[cg], eights, b0[cg], b1[cg]);
         }
 #pragma unroll
         for (int grp = n * F; grp < n * F + F; ++grp) {
-          const uint32_t v0 = w[0][grp] >> 8, v1 = w[1][grp] >> 8;
-          const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[0][grp] & 0x00f000f0u, w[1][grp] & 0x000f000fu, w[1][grp] & 0x00f000f0u};
-          const uint32_t f1[4] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu, v1 & 0x00f000f0u};
+          // rows g + 8 take both codes of a byte, c + 16 c': the rows g are taken off them at the end
+          const uint32_t v0 = high_bytes(w[0][grp]), v1 = high_bytes(w[1][grp]);
+          const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[0][grp] & 0x00ff00ffu, w[1][grp] & 0x000f000fu, w[1][grp] & 0x00ff00ffu};
+          const uint32_t f1[4] = {v0 & 0x000f000fu, v0, v1 & 0x000f000fu, v1};
 #pragma unroll
           for (int cg = 0; cg < NCG; ++cg) {
             mma_f16(acc[cg][grp][0], f0, b0[cg], b1[cg]);
@@ -757,26 +771,26 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
         int hd, tk;
         if (column(cg, 2 * t + j, c0, &hd, &tk)) {
           const int c = (cg * 8 + 2 * t + j) & (C::kCols - 1);
-          const float base2 = limit[cg][j] == -INFINITY ? -INFINITY : -mneg[cg][j];
           const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (row0 + static_cast<size_t>(tk) * a.Hq + hd) * D + 4 * g + 32 * half;
           float* part = slot + c * D + 4 * g + 32 * half;
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
-            // 1 / rinv, exactly; raw numerators are in units of 2^-24 (2^-20: odd channels)
+            // 1 / rinv, exactly; raw numerators are in units of 2^-24 (odd channels: of 2^-20, their neighbour's taken off)
             const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv, less8 = eight[n] * pow2(24);
             float y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float own = half ? acc[cg][F * n + F - 1][i >> 1][j + 2 * (i & 1)] : acc[cg][F * n][i >> 1][j + 2 * (i & 1)];
-              y[i] = fmaf(own, i & 1 ? pow2(20) : pow2(24), -less8) * f;
+              const float(&own)[4] = acc[cg][F * n][i >> 1], (&odd)[4] = acc[cg][F * n + F - 1][i >> 1];
+              const float even = half ? odd[j] : own[j], both = half ? odd[j + 2] : own[j + 2];
+              y[i] = fmaf(i & 1 ? both - even : even, i & 1 ? pow2(20) : pow2(24), -less8) * f;
             }
             if (whole) *reinterpret_cast<uint2*>(o + 32 * F * n) = make_uint2(wm_pack_bf16x2(y[0], y[1]), wm_pack_bf16x2(y[2], y[3]));
             else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);
           }
           if (g == 0 && half == 0) {
-            if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(base2, sum);
-            else if (a.lse) a.lse[(static_cast<size_t>(ub) * a.Hq + uh * heads + hd) * a.Sq + tk] = sum == 0.f ? -INFINITY : (base2 + log2f(sum)) * kLn2;
+            if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(-mneg[cg][j], sum);
+            else if (a.lse) a.lse[(static_cast<size_t>(ub) * a.Hq + uh * heads + hd) * a.Sq + tk] = sum == 0.f ? -INFINITY : (log2f(sum) - mneg[cg][j]) * kLn2;
           }
         }
       }
