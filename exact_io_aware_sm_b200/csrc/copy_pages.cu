@@ -12,6 +12,8 @@ namespace eio {
 namespace {
 
 constexpr int kCopyThreads = 256;
+constexpr int kCopyEach = 4;                            // 16-byte pieces of a thread, all in flight at once
+constexpr int kCopyChunk = kCopyThreads * kCopyEach;  // of a block: 16 KB
 
 template <int N>
 struct Moves {
@@ -20,27 +22,34 @@ struct Moves {
 
 template <int N>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(uint8_t* pool, long long page_bytes, const __grid_constant__ Moves<N> m) {
-  const uint4* from = reinterpret_cast<const uint4*>(pool + m.src[blockIdx.y] * page_bytes);
-  uint4* to = reinterpret_cast<uint4*>(pool + m.dst[blockIdx.y] * page_bytes);
-  const long long n = page_bytes / 16;
-  for (long long i = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * kCopyThreads)
-    to[i] = from[i];
+  const long long n = page_bytes / 16, at = static_cast<long long>(blockIdx.x) * kCopyChunk + threadIdx.x;
+  const uint4* from = reinterpret_cast<const uint4*>(pool + m.src[blockIdx.y] * page_bytes) + at;
+  uint4* to = reinterpret_cast<uint4*>(pool + m.dst[blockIdx.y] * page_bytes) + at;
+  uint4 x[kCopyEach];
+#pragma unroll
+  for (int i = 0; i < kCopyEach; ++i)
+    if (at + i * kCopyThreads < n) x[i] = __ldcs(from + i * kCopyThreads);
+#pragma unroll
+  for (int i = 0; i < kCopyEach; ++i)
+    if (at + i * kCopyThreads < n) __stcs(to + i * kCopyThreads, x[i]);
 }
 
 template <int N>
 cudaError_t launch_n(void* pool, long long page_bytes, const int* src, const int* dst, int n, cudaStream_t s) {
   Moves<N> m;
   for (int i = 0; i < n; ++i) m.src[i] = src[i], m.dst[i] = dst[i];
-  const long long chunks = (page_bytes / 16 + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
-  const dim3 grid(static_cast<unsigned>(chunks < 64 ? chunks : 64), n);
-  copy_pages_kernel<N><<<grid, kCopyThreads, 0, s>>>(static_cast<uint8_t*>(pool), page_bytes, m);
+  const long long chunks = (page_bytes / 16 + kCopyChunk - 1) / kCopyChunk;
+  if (chunks > 0x7fffffffll) return cudaErrorInvalidValue;
+  copy_pages_kernel<N><<<dim3(static_cast<unsigned>(chunks), n), kCopyThreads, 0, s>>>(static_cast<uint8_t*>(pool), page_bytes, m);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+// One launch takes up to 4000 moves (32 KB of parameters are the most); few moves take little ones.
 cudaError_t launch_copy_pages(void* pool, long long page_bytes, const int* src, const int* dst, int n, cudaStream_t s) {
-  constexpr int kMost = 500;  // 4000 bytes of parameters
+  constexpr int kFew = 32, kMost = 4000;
+  if (n <= kFew) return launch_n<kFew>(pool, page_bytes, src, dst, n, s);
   for (int i = 0; i < n; i += kMost) {
     const cudaError_t e = launch_n<kMost>(pool, page_bytes, src + i, dst + i, n - i < kMost ? n - i : kMost, s);
     if (e != cudaSuccess) return e;

@@ -4,8 +4,17 @@
 //     m = max |x|,  s = bf16(m / 7),  c = 8 + floor(x / s + 1/2)
 // kv4_read: (c - 8) * s, rounded once to bf16.
 //
-// Both are memory bound: per token and head 4 d bytes of bf16 rows and
-// d + d / 8 bytes of cache, with about ten instructions a channel pair.
+// One warp a tile of the cache (16 tokens of one head), whatever part of it the
+// call covers: lane (g, t) takes channels 8 t .. 8 t + 7 of every group of tokens
+// g and g + 8, so that rows move in 16-byte pieces (64 contiguous bytes a group and
+// token), codes in 16-byte pieces too, and the maximum of a group needs two shuffles.
+// K's codes are then in place; V's pairs of tokens exchange halves with the lane of
+// the other token.  A token's bytes are its own: a tile that is covered in part
+// is written in part, never read.
+//
+// Both are memory bound: per token and head 4 d bytes of bf16 rows and d + d / 8
+// bytes of cache, with about five instructions a value to narrow and two and a half
+// to widen.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -14,151 +23,223 @@
 namespace eio {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowWarps = 4;
 
-// The tokens that sequence b appends: rows 0 .. n - 1 of the call's k and v, at
-// positions len - n .. len - 1; none (and the error latched) for counts that
-// do not fit the rows, the sequence or the table.
-__device__ __forceinline__ int append_count(const Kv4AppendArgs& a, int b, int* first) {
-  const int len = a.pages.seqlens[b];
-  const int n = a.n_new ? a.n_new[b] : a.N;
-  const long long room = static_cast<long long>(a.pages.max_pages) << a.pages.page_shift;
-  if (n < 0 || n > a.N || len < n || len > room) {
-    atomicCAS(a.pages.err, 0, kErrDeviceArg);
-    return 0;
+// Tiles that n consecutive tokens may touch.
+__host__ __device__ constexpr int tiles_of(int n) { return (n + 14) / 16 + 1; }
+
+struct TileAt {
+  int b, tile, h;  // the tile'th of those that sequence b's tokens touch
+  bool ok;
+};
+
+__device__ __forceinline__ TileAt my_tile(int B, int Hkv, int N) {
+  const long long w = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  const int per = tiles_of(N);
+  const long long bt = w / Hkv;
+  TileAt x;
+  x.h = static_cast<int>(w - bt * Hkv);
+  x.b = static_cast<int>(bt / per);
+  x.tile = static_cast<int>(bt - static_cast<long long>(x.b) * per);
+  x.ok = x.b < B;
+  return x;
+}
+
+// A lane's group words [G] to or from 4 G consecutive bytes.
+template <int G>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t* w) {
+  if constexpr (G == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <int G>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (G == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
   }
-  *first = len - n;
-  return n;
+}
+
+// The codes of eight channels (low nibbles first) of a group, and the group's scale, from four lanes' shares.
+__device__ __forceinline__ uint32_t narrow(const uint4& x, uint32_t* scale) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  m = max(m & 0xffffu, m >> 16);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  *scale = kv4_scale_bits(m);
+  const float inv = kv4_inverse(*scale);
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // infinities and NaNs have inv 0 and code 8 like the rest of their group
+    const float lo = inv == 0.f ? 0.f : __uint_as_float(w[i] << 16), hi = inv == 0.f ? 0.f : __uint_as_float(w[i] & 0xffff0000u);
+    out |= kv4_code(lo, inv) << (8 * i) | kv4_code(hi, inv) << (8 * i + 4);
+  }
+  return out;
+}
+
+// (c - 8) s of eight codes as bf16, rounded once.
+__device__ __forceinline__ uint4 widen(uint32_t w, uint32_t scale) {
+  const uint32_t s2 = scale | scale << 16;
+  uint32_t y[4];  // codes i and i + 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = (w >> (4 * i) & 0x000f000fu) | 0x43004300u;  // 128 + c
+    const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), __floats2bfloat162_rn(136.f, 136.f)),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&s2));
+    y[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4AppendArgs a) {
   constexpr int G = D / 32;
-  const long long total = static_cast<long long>(a.pages.B) * a.N * a.pages.Hkv * G;
-  const long long i = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (i >= total) return;
-  const int grp = static_cast<int>(i % G);
-  const long long row = i / G;
-  const int h = static_cast<int>(row % a.pages.Hkv);
-  const int n = static_cast<int>(row / a.pages.Hkv % a.N), b = static_cast<int>(row / a.pages.Hkv / a.N);
-  int first = 0;
-  if (n >= append_count(a, b, &first)) return;
-  const int pos = first + n, tok = pos & 15;
-  const long long at = kv4_tile_at<D>(a.pages, b, h, pos, kErrDeviceArg);
+  const TileAt x = my_tile(a.pages.B, a.pages.Hkv, a.N);
+  if (!x.ok) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // The tokens that sequence b appends: rows 0 .. n - 1 of k and v, positions len - n .. len - 1.
+  const int len = a.pages.seqlens[x.b];
+  const int n = a.n_new ? a.n_new[x.b] : a.N;
+  if (n < 0 || n > a.N || len < n || len > static_cast<long long>(a.pages.max_pages) << a.pages.page_shift) {
+    if (lane == 0) atomicCAS(a.pages.err, 0, kErrDeviceArg);
+    return;
+  }
+  const int first = len - n, pos0 = (first & ~15) + 16 * x.tile;
+  if (n == 0 || pos0 >= len) return;
+  const long long at = kv4_tile_at<D>(a.pages, x.b, x.h, pos0, kErrDeviceArg);
   if (at < 0) return;
   uint8_t* tile = a.pages.pool + at;
+  uint4 in[2][2][G];  // of K and V, tokens g and g + 8, every group
+  bool live[2];
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(which ? a.v : a.k) +
-                               (which ? b * a.v_sb + n * a.v_sn : b * a.k_sb + n * a.k_sn) + h * D + grp * 32;
-    uint32_t w[16];
-    uint32_t m = 0;
+  for (int r = 0; r < 2; ++r) {
+    const int pos = pos0 + g + 8 * r, i = pos - first;
+    live[r] = i >= 0 && pos < len;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 u = reinterpret_cast<const uint4*>(src)[j];
-      w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
+    for (int which = 0; which < 2; ++which) {
+      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(which ? a.v : a.k) +
+                                 (which ? x.b * a.v_sb + i * a.v_sn : x.b * a.k_sb + i * a.k_sn) + x.h * D + 8 * t;
+#pragma unroll
+      for (int grp = 0; grp < G; ++grp) in[which][r][grp] = live[r] ? *reinterpret_cast<const uint4*>(row + 32 * grp) : make_uint4(0u, 0u, 0u, 0u);
     }
+  }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
-    const uint32_t s = kv4_scale_bits(m);
-    const float inv = kv4_inverse(s);
-    uint32_t out[4];  // eight channels each, low nibble first
+  for (int r = 0; r < 2; ++r) {
+    const int tok = g + 8 * r;
+    uint32_t w[G], s[G];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t o = 0;
+    for (int grp = 0; grp < G; ++grp) w[grp] = narrow(in[0][r][grp], &s[grp]);
+    if (live[r]) {
+      store_words<G>(tile + (tok * 4 + t) * (4 * G), w);
+      if (t == 0) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t x = w[4 * j + k];
-        // a group that holds infinities or NaNs has code 8 everywhere
-        const float lo = inv == 0.f ? 0.f : __uint_as_float(x << 16), hi = inv == 0.f ? 0.f : __uint_as_float(x & 0xffff0000u);
-        o |= kv4_code(lo, inv) << (8 * k) | kv4_code(hi, inv) << (8 * k + 4);
+        for (int i = 0; i < G / 2; ++i) *reinterpret_cast<uint32_t*>(tile + kv4_off_ks(D) + tok * (2 * G) + 4 * i) = s[2 * i] | s[2 * i + 1] << 16;
       }
-      out[j] = o;
     }
-    if (which == 0) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) *reinterpret_cast<uint32_t*>(tile + tok * (D / 2) + t * (4 * G) + grp * 4) = out[t];
-    } else {
-      uint8_t* v = tile + kv4_off_v(D) + (tok >> 3) * (4 * D) + ((tok & 7) >> 1) * (4 * G) + grp * 4 + (tok & 1) * 2;
+    for (int grp = 0; grp < G; ++grp) w[grp] = narrow(in[1][r][grp], &s[grp]);
+    if (live[r] && t == 1) {
 #pragma unroll
-      for (int g = 0; g < 8; ++g) *reinterpret_cast<uint16_t*>(v + g * (16 * G)) = static_cast<uint16_t>(out[g >> 1] >> (16 * (g & 1)));
+      for (int i = 0; i < G / 2; ++i) *reinterpret_cast<uint32_t*>(tile + kv4_off_vs(D) + tok * (2 * G) + 4 * i) = s[2 * i] | s[2 * i + 1] << 16;
     }
-    *reinterpret_cast<uint16_t*>(tile + (which ? kv4_off_vs(D) : kv4_off_ks(D)) + tok * (2 * G) + grp * 2) = static_cast<uint16_t>(s);
+    // The lane of an even token takes channels 8 t .. 8 t + 3 of both tokens of the pair, that of the odd one the rest.
+    const int odd = g & 1;
+    const bool other = __shfl_xor_sync(0xffffffffu, live[r], 4);
+#pragma unroll
+    for (int grp = 0; grp < G; ++grp) {
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, w[grp], 4);
+      w[grp] = odd ? __byte_perm(y, w[grp], 0x7632) : __byte_perm(w[grp], y, 0x5410);
+    }
+    uint8_t* v = tile + kv4_off_v(D) + r * (4 * D) + ((2 * t + odd) * 4 + (g >> 1)) * (4 * G);
+    if (live[r] && other) {
+      store_words<G>(v, w);
+    } else if (live[r] || other) {
+      const int hi = odd ? live[r] : other;  // the odd token is the one that is appended
+#pragma unroll
+      for (int grp = 0; grp < G; ++grp) *reinterpret_cast<uint16_t*>(v + 4 * grp + 2 * hi) = static_cast<uint16_t>(w[grp] >> (16 * hi));
+    }
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const Kv4ReadArgs a) {
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4ReadArgs a) {
   constexpr int G = D / 32;
-  const long long total = static_cast<long long>(a.pages.B) * a.N * a.pages.Hkv * G;
-  const long long i = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (i >= total) return;
-  const int grp = static_cast<int>(i % G);
-  const long long row = i / G;
-  const int h = static_cast<int>(row % a.pages.Hkv);
-  const int n = static_cast<int>(row / a.pages.Hkv % a.N), b = static_cast<int>(row / a.pages.Hkv / a.N);
-  const long long room = static_cast<long long>(a.pages.max_pages) << a.pages.page_shift;
-  int len = a.pages.seqlens[b], start = a.start ? a.start[b] : 0;
-  if (len < 0 || len > room || start < 0) {
-    atomicCAS(a.pages.err, 0, kErrDeviceArg);
+  const TileAt x = my_tile(a.pages.B, a.pages.Hkv, a.N);
+  if (!x.ok) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  int len = a.pages.seqlens[x.b], start = a.start ? a.start[x.b] : 0;
+  if (len < 0 || len > static_cast<long long>(a.pages.max_pages) << a.pages.page_shift || start < 0) {
+    if (lane == 0) atomicCAS(a.pages.err, 0, kErrDeviceArg);
     len = 0;
     start = 0;
   }
-  const long long pos = static_cast<long long>(start) + n;
-  const long long at = pos < len ? kv4_tile_at<D>(a.pages, b, h, static_cast<int>(pos), kErrDeviceArg) : -1;
-  const int tok = static_cast<int>(pos & 15);
+  const long long pos0 = (static_cast<long long>(start) & ~15ll) + 16 * x.tile;
+  const long long at = pos0 < len ? kv4_tile_at<D>(a.pages, x.b, x.h, static_cast<int>(pos0), kErrDeviceArg) : -1;
   const uint8_t* tile = a.pages.pool + (at < 0 ? 0 : at);
+  const int odd = g & 1;
+  uint32_t w[2][2][G], s[2][2][G / 2];  // of K and V, tokens g and g + 8
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(which ? a.v : a.k) + row * D + grp * 32);
-    uint32_t w[4] = {0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
-    float s = 0.f;
-    if (at >= 0) {
-      const uint16_t sb = *reinterpret_cast<const uint16_t*>(tile + (which ? kv4_off_vs(D) : kv4_off_ks(D)) + tok * (2 * G) + grp * 2);
-      s = __uint_as_float(static_cast<uint32_t>(sb) << 16);
-      if (which == 0) {
+  for (int r = 0; r < 2; ++r) {
+    const int tok = g + 8 * r;
+    const bool live = at >= 0 && pos0 + tok < len;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint32_t*>(tile + tok * (D / 2) + t * (4 * G) + grp * 4);
-      } else {
-        const uint8_t* v = tile + kv4_off_v(D) + (tok >> 3) * (4 * D) + ((tok & 7) >> 1) * (4 * G) + grp * 4 + (tok & 1) * 2;
-#pragma unroll
-        for (int g = 0; g < 8; g += 2)
-          w[g >> 1] = *reinterpret_cast<const uint16_t*>(v + g * (16 * G)) |
-                      static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(v + (g + 1) * (16 * G))) << 16;
-      }
+    for (int i = 0; i < G / 2; ++i) {
+      s[0][r][i] = live ? *reinterpret_cast<const uint32_t*>(tile + kv4_off_ks(D) + tok * (2 * G) + 4 * i) : 0u;
+      s[1][r][i] = live ? *reinterpret_cast<const uint32_t*>(tile + kv4_off_vs(D) + tok * (2 * G) + 4 * i) : 0u;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint4 u;
-      __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(&u);
+    for (int i = 0; i < G; ++i) w[0][r][i] = w[1][r][i] = 0x88888888u;
+    if (at >= 0) {
+      load_words<G>(tile + (tok * 4 + t) * (4 * G), w[0][r]);
+      load_words<G>(tile + kv4_off_v(D) + r * (4 * D) + ((2 * t + odd) * 4 + (g >> 1)) * (4 * G), w[1][r]);
+    }
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float lo = static_cast<float>(static_cast<int>((w[j] >> (8 * k)) & 15u) - 8);
-        const float hi = static_cast<float>(static_cast<int>((w[j] >> (8 * k + 4)) & 15u) - 8);
-        o[k] = __floats2bfloat162_rn(lo * s, hi * s);
+  for (int r = 0; r < 2; ++r) {
+#pragma unroll
+    for (int grp = 0; grp < G; ++grp) {  // V: back from half the channels of two tokens to all of one
+      uint32_t& v = w[1][r][grp];
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, v, 4);
+      v = odd ? __byte_perm(y, v, 0x7632) : __byte_perm(v, y, 0x5410);
+    }
+    const long long i = pos0 + g + 8 * r - start;  // row of the output
+    if (i < 0 || i >= a.N) continue;
+    const long long row = ((static_cast<long long>(x.b) * a.N + i) * a.pages.Hkv + x.h) * D + 8 * t;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(which ? a.v : a.k) + row);
+#pragma unroll
+      for (int grp = 0; grp < G; ++grp) {
+        const uint32_t pair = s[which][r][grp >> 1];
+        out[4 * grp] = widen(w[which][r][grp], grp & 1 ? pair >> 16 : pair & 0xffffu);
       }
-      dst[j] = u;
     }
   }
 }
 
 template <typename A>
-unsigned row_blocks(const A& a, int d) {
-  const long long total = static_cast<long long>(a.pages.B) * a.N * a.pages.Hkv * (d / 32);
-  return static_cast<unsigned>((total + kRowThreads - 1) / kRowThreads);
+unsigned row_blocks(const A& a) {
+  const long long warps = static_cast<long long>(a.pages.B) * tiles_of(a.N) * a.pages.Hkv;
+  return static_cast<unsigned>((warps + kRowWarps - 1) / kRowWarps);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(int d, const Kv4AppendArgs& a, cudaStream_t s) {
-  if (d == 64) kv4_append_kernel<64><<<row_blocks(a, d), kRowThreads, 0, s>>>(a);
-  else kv4_append_kernel<128><<<row_blocks(a, d), kRowThreads, 0, s>>>(a);
+  if (d == 64) kv4_append_kernel<64><<<row_blocks(a), kRowWarps * 32, 0, s>>>(a);
+  else kv4_append_kernel<128><<<row_blocks(a), kRowWarps * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_read(int d, const Kv4ReadArgs& a, cudaStream_t s) {
-  if (d == 64) kv4_read_kernel<64><<<row_blocks(a, d), kRowThreads, 0, s>>>(a);
-  else kv4_read_kernel<128><<<row_blocks(a, d), kRowThreads, 0, s>>>(a);
+  if (d == 64) kv4_read_kernel<64><<<row_blocks(a), kRowWarps * 32, 0, s>>>(a);
+  else kv4_read_kernel<128><<<row_blocks(a), kRowWarps * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 

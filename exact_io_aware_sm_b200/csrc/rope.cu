@@ -15,8 +15,8 @@
 //
 // Memory bound: q and k are read and written once.  A block takes a run of
 // tokens; it computes the cosines and sines of its (token, pair)s once into
-// shared memory, then its threads stream over (token, head, eight pairs) with
-// 16-byte loads and stores.
+// shared memory (for every head), then its threads stream over (token, head,
+// eight pairs) with 16-byte loads and stores, four such pieces of work in flight.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -25,10 +25,6 @@ namespace eio {
 namespace {
 
 constexpr int kRopeThreads = 256;
-
-struct Pairs8 {
-  float a[8], b[8];
-};
 
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
@@ -48,112 +44,157 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return u;
 }
 
-// The 16 channels of eight pairs as two runs of eight: lo and hi halves of a
-// head, or (interleaved) one run of 16.
+// The 16 channels of eight pairs, as read: two runs of eight, the lo and hi halves of a head or
+// (interleaved) one run of 16.
 template <typename T>
-__device__ __forceinline__ void load_runs(const T* lo, const T* hi, float* a, float* b) {
+struct Piece {
+  static constexpr int kWords = sizeof(T) / 2;  // uint4 of a run
+  uint4 lo[kWords], hi[kWords];
+};
+
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* lo, const T* hi, Piece<T>& p) {
+#pragma unroll
+  for (int i = 0; i < Piece<T>::kWords; ++i) {
+    p.lo[i] = __ldcs(reinterpret_cast<const uint4*>(lo) + i);
+    p.hi[i] = __ldcs(reinterpret_cast<const uint4*>(hi) + i);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void open_run(const uint4* u, float* f) {
   if constexpr (sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(lo), v = *reinterpret_cast<const uint4*>(hi);
-    unpack8(u, a);
-    unpack8(v, b);
+    unpack8(u[0], f);
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 u = *reinterpret_cast<const float4*>(lo + 4 * i), v = *reinterpret_cast<const float4*>(hi + 4 * i);
-      a[4 * i] = u.x, a[4 * i + 1] = u.y, a[4 * i + 2] = u.z, a[4 * i + 3] = u.w;
-      b[4 * i] = v.x, b[4 * i + 1] = v.y, b[4 * i + 2] = v.z, b[4 * i + 3] = v.w;
+      f[4 * i] = __uint_as_float(u[i].x), f[4 * i + 1] = __uint_as_float(u[i].y);
+      f[4 * i + 2] = __uint_as_float(u[i].z), f[4 * i + 3] = __uint_as_float(u[i].w);
     }
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void store_runs(T* lo, T* hi, const float* a, const float* b) {
+__device__ __forceinline__ void store_run(T* p, const float* f) {
   if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(lo) = pack8(a);
-    *reinterpret_cast<uint4*>(hi) = pack8(b);
+    *reinterpret_cast<uint4*>(p) = pack8(f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      *reinterpret_cast<float4*>(lo + 4 * i) = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
-      *reinterpret_cast<float4*>(hi + 4 * i) = make_float4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
-    }
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(p + 4 * i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
   }
 }
 
-template <typename T, bool INTERLEAVED>
+template <typename T>
+constexpr int kRopeEach = sizeof(T) == 2 ? 4 : 2;  // pieces of work that a thread has in flight: 128 bytes
+
+struct RopeOffsets {
+  long long q, k, qo, ko;  // of a token's first head
+};
+
+template <typename T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  extern __shared__ float2 cs[];  // [tokens of the block][pairs, rounded up to 8]
-  const int chunks = a.d / 16, half = a.d / 2;
-  const int padded = chunks * 8;
-  const long long tokens = static_cast<long long>(a.B) * a.N;
-  const long long first = static_cast<long long>(blockIdx.x) * a.tokens_per_block;
-  const int nt = static_cast<int>(min(static_cast<long long>(a.tokens_per_block), tokens - first));
+  constexpr int kEach = kRopeEach<T>;
+  constexpr int kChunks = D / 16, kHalf = D / 2;  // pieces of eight pairs, pairs of a head
+  // Cosine and sine: two pairs of chunk c at [token][pair / 2 % 4][c], so that the chunks' reads are consecutive.
+  extern __shared__ float4 cs[];
+  RopeOffsets* offs = reinterpret_cast<RopeOffsets*>(cs + a.tokens_per_block * (kHalf / 2));
+  const int first = static_cast<int>(blockIdx.x) * a.tokens_per_block;
+  const int nt = min(a.tokens_per_block, a.B * a.N - first);
 
-  for (int i = threadIdx.x; i < nt * padded; i += kRopeThreads) {
-    const int t = i / padded, p = i % padded;
+  for (int i = threadIdx.x; i < nt * kHalf; i += kRopeThreads) {
+    const int t = i / kHalf, p = i % kHalf;
     float s = 0.f, c = 1.f;
     if (p < a.n_pairs) {
-      const long long tok = first + t;
-      const long long pos = a.positions[tok / a.N * a.p_sb + tok % a.N * a.p_sn + a.axis[p]];
+      const int b = (first + t) / a.N, n = first + t - b * a.N;
+      const long long pos = a.positions[b * a.p_sb + n * a.p_sn + a.axis[p]];
       const unsigned long long turns = static_cast<unsigned long long>(pos) * a.freq[p];
       sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
       if (a.inverse) s = -s;
     }
-    cs[i] = make_float2(c, s);
+    reinterpret_cast<float2*>(cs)[2 * (t * (kHalf / 2) + p % 8 / 2 * kChunks + p / 8) + p % 2] = make_float2(c, s);
+  }
+  if (threadIdx.x < nt) {
+    const int b = (first + threadIdx.x) / a.N, n = first + threadIdx.x - b * a.N;
+    offs[threadIdx.x] = RopeOffsets{b * a.q_sb + n * a.q_sn, b * a.k_sb + n * a.k_sn, b * a.qo_sb + n * a.qo_sn, b * a.ko_sb + n * a.ko_sn};
   }
   __syncthreads();
 
-  const int heads = a.Hq + a.Hk;
-  const int items = nt * heads * chunks;
-  for (int i = threadIdx.x; i < items; i += kRopeThreads) {
-    const int chunk = i % chunks, row = i / chunks;
-    const int t = row / heads, h = row % heads;
-    const long long tok = first + t;
-    const long long b = tok / a.N, n = tok % a.N;
-    const bool isq = h < a.Hq;
-    const long long in_at = isq ? b * a.q_sb + n * a.q_sn + h * a.d : b * a.k_sb + n * a.k_sn + (h - a.Hq) * a.d;
-    const long long out_at = isq ? b * a.qo_sb + n * a.qo_sn + h * a.d : b * a.ko_sb + n * a.ko_sn + (h - a.Hq) * a.d;
-    const T* in = static_cast<const T*>(isq ? a.q : a.k) + in_at;
-    T* out = static_cast<T*>(isq ? a.q_out : a.k_out) + out_at;
-    const int lo = INTERLEAVED ? 16 * chunk : 8 * chunk, hi = INTERLEAVED ? 16 * chunk + 8 : half + 8 * chunk;
-    float x[8], y[8];
-    load_runs(in + lo, in + hi, x, y);
-    const float2* w = cs + t * padded + 8 * chunk;
-    if constexpr (INTERLEAVED) {
+  const int heads = a.Hq + a.Hk, items = nt * heads * kChunks;
+  const int chunk = threadIdx.x % kChunks;  // kRopeThreads is a multiple of kChunks: the same for all of a thread's items
+  const int lo = INTERLEAVED ? 16 * chunk : 8 * chunk, hi = INTERLEAVED ? 16 * chunk + 8 : kHalf + 8 * chunk;
+  for (int i0 = threadIdx.x; i0 < items; i0 += kEach * kRopeThreads) {
+    Piece<T> piece[kEach];
+    T* out[kEach];
+    int tok[kEach];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float* r = j < 4 ? x + 2 * j : y + 2 * j - 8;
-        const float u = r[0], v = r[1];
-        r[0] = u * w[j].x - v * w[j].y;
-        r[1] = u * w[j].y + v * w[j].x;
+    for (int e = 0; e < kEach; ++e) {
+      const int i = i0 + e * kRopeThreads;
+      if (i >= items) break;
+      const int row = i / kChunks, t = row / heads, h = row - t * heads;
+      const RopeOffsets& at = offs[t];
+      tok[e] = t;
+      const T* in;
+      if (h < a.Hq) {
+        in = static_cast<const T*>(a.q) + at.q + h * D;
+        out[e] = static_cast<T*>(a.q_out) + at.qo + h * D;
+      } else {
+        in = static_cast<const T*>(a.k) + at.k + (h - a.Hq) * D;
+        out[e] = static_cast<T*>(a.k_out) + at.ko + (h - a.Hq) * D;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = x[j], v = y[j];
-        x[j] = u * w[j].x - v * w[j].y;
-        y[j] = u * w[j].y + v * w[j].x;
-      }
+      load_piece(in + lo, in + hi, piece[e]);
     }
-    store_runs(out + lo, out + hi, x, y);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (i0 + e * kRopeThreads >= items) break;
+      float x[8], y[8];
+      open_run<T>(piece[e].lo, x);
+      open_run<T>(piece[e].hi, y);
+      const float4* w = cs + tok[e] * (kHalf / 2) + chunk;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 r = w[j * kChunks];  // pairs 2 j and 2 j + 1
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float c = k ? r.z : r.x, s = k ? r.w : r.y;
+          const int p = 2 * j + k;
+          float& u = INTERLEAVED ? (p < 4 ? x[(2 * p) & 7] : y[(2 * p) & 7]) : x[p];
+          float& v = INTERLEAVED ? (p < 4 ? x[(2 * p + 1) & 7] : y[(2 * p + 1) & 7]) : y[p];
+          const float u0 = u, v0 = v;
+          u = u0 * c - v0 * s;
+          v = u0 * s + v0 * c;
+        }
+      }
+      store_run(out[e] + lo, x);
+      store_run(out[e] + hi, y);
+    }
   }
 }
 
-template <typename T, bool INTERLEAVED>
-cudaError_t launch_t(const RopeArgs& a, cudaStream_t s) {
-  const long long tokens = static_cast<long long>(a.B) * a.N;
-  const long long blocks = (tokens + a.tokens_per_block - 1) / a.tokens_per_block;
-  const size_t smem = static_cast<size_t>(a.tokens_per_block) * (a.d / 2) * sizeof(float2);
-  rope_kernel<T, INTERLEAVED><<<static_cast<unsigned>(blocks), kRopeThreads, smem, s>>>(a);
+template <typename T, int D>
+cudaError_t launch_t(bool interleaved, const RopeArgs& a, cudaStream_t s) {
+  const int tokens = a.B * a.N;
+  const int blocks = (tokens - 1) / a.tokens_per_block + 1;
+  const size_t smem = static_cast<size_t>(a.tokens_per_block) * (D / 2 * sizeof(float2) + sizeof(RopeOffsets));
+  if (interleaved) rope_kernel<T, D, true><<<blocks, kRopeThreads, smem, s>>>(a);
+  else rope_kernel<T, D, false><<<blocks, kRopeThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+// Tokens of a block: one round of its threads' pieces where there are blocks enough for every SM to hold
+// four, fewer tokens where there are not.
 cudaError_t launch_rope(bool bf16, bool interleaved, RopeArgs a, cudaStream_t s) {
-  a.tokens_per_block = 4;
-  if (bf16) return interleaved ? launch_t<__nv_bfloat16, true>(a, s) : launch_t<__nv_bfloat16, false>(a, s);
-  return interleaved ? launch_t<float, true>(a, s) : launch_t<float, false>(a, s);
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  const long long per_token = static_cast<long long>(a.Hq + a.Hk) * (a.d / 16);
+  long long each = kRopeThreads * (bf16 ? kRopeEach<__nv_bfloat16> : kRopeEach<float>) / per_token;
+  if (each > tokens / (4 * 148)) each = tokens / (4 * 148);
+  a.tokens_per_block = each < 1 ? 1 : each > 16 ? 16 : static_cast<int>(each);
+  switch (a.d) {
+    case 32: return bf16 ? launch_t<__nv_bfloat16, 32>(interleaved, a, s) : launch_t<float, 32>(interleaved, a, s);
+    case 64: return bf16 ? launch_t<__nv_bfloat16, 64>(interleaved, a, s) : launch_t<float, 64>(interleaved, a, s);
+    default: return bf16 ? launch_t<__nv_bfloat16, 128>(interleaved, a, s) : launch_t<float, 128>(interleaved, a, s);
+  }
 }
 
 }  // namespace eio
