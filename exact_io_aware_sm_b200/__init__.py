@@ -35,10 +35,11 @@ being written or read past its end.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 
 import numpy as np
 
@@ -296,33 +297,55 @@ def attn_decode_multi(q, k_cache, v_cache, seqlens, o=None, lse=None, scale=None
 
 
 def _on(stream):
-    """The context that allocates a call's outputs and workspace on the stream that
-    the call runs on (so that their memory is not reused while it runs)."""
+    """The context that makes `stream` the current one, so that a call's outputs and workspace
+    belong to the stream it runs on (their memory is not reused while it runs)."""
     import torch
-    if stream is None:
-        return contextlib.nullcontext()
     if stream.device_index != torch.cuda.current_device():
         raise ValueError(f"stream is on device {stream.device_index} but the current CUDA device is "
                          f"{torch.cuda.current_device()}")
     return torch.cuda.stream(stream)
 
 
-def _need_rows(t, name, shape, dtype, device=None):
-    """_need for a [B, N, H, d] tensor whose heads and channels are contiguous but whose
-    batch and token strides are free (a part of a fused projection); returns those two
-    strides (0 for dimensions of one element)."""
+def _stream_here(device):
+    """The current stream of the current device as an integer handle."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _is(t, shape, dtype, device):
+    """Whether a tensor is what the library takes; the calls below ask this first and _need, which
+    says what is wrong, only where it is not (small calls are bound by the host)."""
+    return t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device
+
+
+def _device_of(t, name):
+    """The current device, on which the call's first tensor has to be."""
+    import torch
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected 4 dimensions")
+    device, cur = t.get_device(), torch.cuda.current_device()
+    if device != cur:
+        raise ValueError(f"{name} is on {t.device} but the current CUDA device is {cur}; "
+                         f"call inside torch.cuda.device({device})")
+    return device
+
+
+def _rows(t, name, shape, dtype, device):
+    """Check a [B, N, H, d] tensor whose heads and channels are contiguous but whose batch and
+    token strides are free (a part of a fused projection); returns those two strides (0 for
+    dimensions of one element)."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}; expected cuda:{device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected {dtype}")
+    if t.dim() != 4 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape or ('*',) * 4)}")
     B, N, H, d = t.shape
     sb, sn, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (H > 1 and sh != d):
         raise ValueError(f"{name} must have contiguous heads and channels (strides {t.stride()})")
-    if t.numel():
-        _need(t[:1, :1], name, (1, 1, H, d), (dtype,), device)
-    if any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple('*' if w is None else w for w in shape)}")
     return (sb if B > 1 else 0), (sn if N > 1 else 0)
 
 
@@ -359,6 +382,9 @@ def _apart(out, name, others):
         raise ValueError(f"{name} overlaps another tensor of the call")
 
 
+_PACK10, _PACK4 = struct.Struct("10q").pack, struct.Struct("4q").pack  # strides, as the library reads them
+
+
 def rope(q, k, positions, axes, freq, interleaved=False, inverse=False, q_out=None, k_out=None, stream=None):
     """Rotary positions with several axes.  q [B,N,Hq,d], k [B,N,Hk,d] (or None), bf16 or
     fp32; positions int32 [B,N,A] (or [N,A] for every sequence); axes and freq: host
@@ -367,52 +393,57 @@ def rope(q, k, positions, axes, freq, interleaved=False, inverse=False, q_out=No
     entry are copied.  inverse rotates back.  q and k may have any batch and token
     strides of whole 16 bytes; q_out may be q, and k_out k.  Returns (q_out, k_out)."""
     import torch
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"q has dtype {q.dtype}; expected torch.bfloat16 or torch.float32")
-    qs = _need_rows(q, "q", (None,) * 4, q.dtype)
+    if stream is not None:
+        with _on(stream):
+            return rope(q, k, positions, axes, freq, interleaved, inverse, q_out, k_out)
+    dev, dtype = _device_of(q, "q"), q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"q has dtype {dtype}; expected torch.bfloat16 or torch.float32")
+    qb, qn = _rows(q, "q", None, dtype, dev)
     B, N, Hq, d = q.shape
-    ks, Hk = (0, 0), 0
+    kb = kn = kob = kon = Hk = 0
     if k is not None:
-        ks = _need_rows(k, "k", (B, N, None, d), q.dtype, q.device)
-        Hk = k.shape[2]
-    axes = np.ascontiguousarray(axes, dtype=np.uint8)
-    freq = np.ascontiguousarray(freq, dtype=np.float64)
+        Hk = k.shape[2] if k.dim() == 4 else 0
+        kb, kn = _rows(k, "k", (B, N, Hk, d), dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if not q.numel() or (k is not None and not Hk):
+        raise ValueError(f"q and k must not be empty, got {tuple(q.shape)}" + ("" if k is None else f" and {tuple(k.shape)}"))
+    axes = np.asarray(axes, dtype=np.uint8)
+    freq = np.asarray(freq, dtype=np.float64)
     if axes.ndim != 1 or axes.shape != freq.shape:
         raise ValueError(f"axes and freq must be vectors of one length, got {axes.shape} and {freq.shape}")
+    if not (getattr(positions, "is_cuda", False) and positions.dtype is torch.int32 and positions.get_device() == dev):
+        raise ValueError(f"positions must be an int32 tensor on cuda:{dev}")
     if positions.dim() == 2:
         positions = positions.expand(B, *positions.shape)
-    if positions.dim() != 3 or tuple(positions.shape[:2]) != (B, N):
+    if positions.dim() != 3 or positions.shape[0] != B or positions.shape[1] != N:
         raise ValueError(f"positions has shape {tuple(positions.shape)}; expected ({B}, {N}, *) or ({N}, *)")
     A = positions.shape[2]
-    if A > 1 and positions.stride(2) != 1:
+    pb, pn, pa = positions.stride()
+    if A > 1 and pa != 1:
         raise ValueError("positions must be contiguous in its last dimension")
-    if positions.numel():
-        _need(positions[:1, :1], "positions", (1, 1, A), (torch.int32,), q.device)
-    ps = (positions.stride(0) if B > 1 else 0), (positions.stride(1) if N > 1 else 0)
-    with _on(stream):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if q_out is None:
+        q_out = torch.empty((B, N, Hq, d), dtype=dtype, device=q.device)
+        qob, qon = N * Hq * d, Hq * d
+    else:
+        qob, qon = _rows(q_out, "q_out", (B, N, Hq, d), dtype, dev)
+        _apart(q_out, "q_out", [(q, True), (positions, False)] + ([] if k is None else [(k, False)]))
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((B, N, Hk, d), dtype=dtype, device=q.device)
+            kob, kon = N * Hk * d, Hk * d
         else:
-            _apart(q_out, "q_out", [(q, True), (positions, False)] + ([(k, False)] if k is not None else []))
-        if k_out is None and k is not None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        elif k is not None:
+            kob, kon = _rows(k_out, "k_out", (B, N, Hk, d), dtype, dev)
             _apart(k_out, "k_out", [(k, True), (q, False), (q_out, False), (positions, False)])
-        elif k_out is not None:
-            raise ValueError("k_out without k")
-    qo = _need_rows(q_out, "q_out", q.shape, q.dtype, q.device)
-    ko = _need_rows(k_out, "k_out", k.shape, q.dtype, q.device) if k is not None else (0, 0)
-    if q.numel() == 0 or (k is not None and k.numel() == 0):
-        raise ValueError(f"q and k must not be empty, got {tuple(q.shape)}" + (f" and {tuple(k.shape)}" if k is not None else ""))
-    strides = (ctypes.c_int64 * 10)(*qs, *ks, *qo, *ko, *ps)
-    _check(lib().attn_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                           None if k is None else k_out.data_ptr(), positions.data_ptr(), _np_ptr(axes),
-                           _np_ptr(freq), strides, B, N, Hq, Hk, d, A, len(axes), int(interleaved), int(inverse),
-                           BF16 if q.dtype == torch.bfloat16 else F32, _stream_ptr(stream)))
+    strides = _PACK10(qb, qn, kb, kn, qob, qon, kob, kon, pb if B > 1 else 0, pn if N > 1 else 0)
+    rc = lib().attn_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                         None if k is None else k_out.data_ptr(), positions.data_ptr(), axes.tobytes(),
+                         freq.tobytes(), strides, B, N, Hq, Hk, d, A, len(axes), bool(interleaved), bool(inverse),
+                         BF16 if dtype is torch.bfloat16 else F32, _stream_here(dev))
+    if rc:
+        _check(rc)
     return q_out, k_out
-
-
-KV4_GROUP = 32  # channels that share a scale
 
 
 def kv4_page_bytes(page, Hkv, d):
@@ -432,16 +463,33 @@ def kv4_pool(n_pages, Hkv, d, page=64, device=None):
 def _kv4(pool, table, seqlens, B, Hkv, d, device):
     """Check a pool, page table and lengths; returns (n_pages, Hkv, page, max_pages)."""
     import torch
-    _need(pool, "pool", (None, Hkv, None), (torch.uint8,), device)
-    _need(table, "table", (B, None), (torch.int32,), pool.device)
-    _need(seqlens, "seqlens", (table.shape[0],), (torch.int32,), pool.device)
-    n_pages, heads, nbytes = pool.shape
+    u8, i32 = torch.uint8, torch.int32
+    if pool.dim() == 3 and table.dim() == 2:
+        n_pages, heads, nbytes = pool.shape
+        rows, max_pages = table.shape
+        ok = (_is(pool, (n_pages, heads, nbytes), u8, device) and _is(table, (rows, max_pages), i32, device)
+              and _is(seqlens, (rows,), i32, device))
+    if pool.dim() != 3 or table.dim() != 2 or not ok or (B or rows) != rows or (Hkv or heads) != heads:
+        dev = torch.device("cuda", device)
+        _need(pool, "pool", (None, Hkv, None), (u8,), dev)
+        _need(table, "table", (B, None), (i32,), dev)
+        _need(seqlens, "seqlens", (table.shape[0],), (i32,), dev)
     if d not in (64, 128):
         raise ValueError(f"the 4-bit cache needs d in (64, 128), got {d}")
     page = nbytes // (18 * d) * 16
     if page not in (16, 32, 64, 128, 256) or nbytes != page // 16 * 18 * d:
         raise ValueError(f"pool has {nbytes} bytes a page and head: no page of 16, 32, 64, 128 or 256 tokens at d = {d}")
-    return n_pages, heads, page, table.shape[1]
+    return n_pages, heads, page, max_pages
+
+
+def _counts(t, name, B, device):
+    """The address of an optional int32 [B] on the device."""
+    import torch
+    if t is None:
+        return None
+    if not _is(t, (B,), torch.int32, device):
+        _need(t, name, (B,), (torch.int32,), torch.device("cuda", device))
+    return t.data_ptr()
 
 
 def kv4_append(k, v, pool, table, seqlens, n_new=None, stream=None):
@@ -450,17 +498,19 @@ def kv4_append(k, v, pool, table, seqlens, n_new=None, stream=None):
     tokens seqlens[b] - n_new[b] .. seqlens[b] - 1; n_new int32 [B] (None: N each), rows
     behind it are padding.  Nothing else in the pool changes.  Returns pool."""
     import torch
-    ks = _need_rows(k, "k", (None,) * 4, torch.bfloat16)
+    if stream is not None:
+        with _on(stream):
+            return kv4_append(k, v, pool, table, seqlens, n_new)
+    dev = _device_of(k, "k")
+    kb, kn = _rows(k, "k", None, torch.bfloat16, dev)
     B, N, Hkv, d = k.shape
-    vs = _need_rows(v, "v", k.shape, torch.bfloat16, k.device)
-    n_pages, _, page, max_pages = _kv4(pool, table, seqlens, B, Hkv, d, k.device)
-    if n_new is not None:
-        _need(n_new, "n_new", (B,), (torch.int32,), k.device)
-    with _on(stream):
-        strides = (ctypes.c_int64 * 4)(*ks, *vs)
-        _check(lib().attn_kv4_append(k.data_ptr(), v.data_ptr(), pool.data_ptr(), table.data_ptr(),
-                                     seqlens.data_ptr(), None if n_new is None else n_new.data_ptr(), strides, B, N,
-                                     Hkv, d, n_pages, page, max_pages, _stream_ptr(stream)))
+    vb, vn = _rows(v, "v", (B, N, Hkv, d), torch.bfloat16, dev)
+    n_pages, _, page, max_pages = _kv4(pool, table, seqlens, B, Hkv, d, dev)
+    rc = lib().attn_kv4_append(k.data_ptr(), v.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(),
+                               _counts(n_new, "n_new", B, dev), _PACK4(kb, kn, vb, vn), B, N, Hkv, d, n_pages, page,
+                               max_pages, _stream_here(dev))
+    if rc:
+        _check(rc)
     return pool
 
 
@@ -468,21 +518,32 @@ def kv4_read(pool, table, seqlens, N, d, start=None, k=None, v=None, stream=None
     """Tokens start[b] .. start[b] + N - 1 (start int32 [B]; None: 0) of each sequence of a
     4-bit cache as bf16 k, v [B,N,Hkv,d]; rows at and past seqlens[b] are zeros."""
     import torch
-    n_pages, Hkv, page, max_pages = _kv4(pool, table, seqlens, None, None, d, None)
+    if stream is not None:
+        with _on(stream):
+            return kv4_read(pool, table, seqlens, N, d, start, k, v)
+    dev = _device_of(pool, "pool")
+    n_pages, Hkv, page, max_pages = _kv4(pool, table, seqlens, None, None, d, dev)
     B = table.shape[0]
-    if start is not None:
-        _need(start, "start", (B,), (torch.int32,), pool.device)
-    with _on(stream):
-        if k is None:
-            k = torch.empty((B, N, Hkv, d), dtype=torch.bfloat16, device=pool.device)
-        if v is None:
-            v = torch.empty((B, N, Hkv, d), dtype=torch.bfloat16, device=pool.device)
-        _need(k, "k", (B, N, Hkv, d), (torch.bfloat16,), pool.device)
-        _need(v, "v", (B, N, Hkv, d), (torch.bfloat16,), pool.device)
-        _check(lib().attn_kv4_read(k.data_ptr(), v.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(),
-                                   None if start is None else start.data_ptr(), B, N, Hkv, d, n_pages, page,
-                                   max_pages, _stream_ptr(stream)))
+    shape, bf16 = (B, N, Hkv, d), torch.bfloat16
+    if k is None:
+        k = torch.empty(shape, dtype=bf16, device=pool.device)
+    elif not _is(k, shape, bf16, dev):
+        _need(k, "k", shape, (bf16,), pool.device)
+    if v is None:
+        v = torch.empty(shape, dtype=bf16, device=pool.device)
+    elif not _is(v, shape, bf16, dev):
+        _need(v, "v", shape, (bf16,), pool.device)
+    rc = lib().attn_kv4_read(k.data_ptr(), v.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(),
+                             _counts(start, "start", B, dev), B, N, Hkv, d, n_pages, page, max_pages,
+                             _stream_here(dev))
+    if rc:
+        _check(rc)
     return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_kv4_workspace(*sizes):
+    return max(0, lib().attn_decode_kv4_workspace(*sizes))  # -1: refused sizes, which the call itself reports
 
 
 def attn_decode_kv4(q, pool, table, seqlens, o=None, lse=None, scale=None, stream=None, want_lse=True):
@@ -490,27 +551,31 @@ def attn_decode_kv4(q, pool, table, seqlens, o=None, lse=None, scale=None, strea
     [B,Sq,Hq,d] bf16; pool from kv4_pool; table int32 [B,max_pages]; seqlens int32 [B]
     on the device (including the Sq new tokens).  Returns o [B,Sq,Hq,d] and lse [B,Hq,Sq]."""
     import torch
-    _need(q, "q", (None,) * 4, (torch.bfloat16,))
-    B, Sq, Hq, d = q.shape
-    n_pages, Hkv, page, max_pages = _kv4(pool, table, seqlens, B, None, d, q.device)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    L = lib()
-    with _on(stream):
-        if o is None:
-            o = torch.empty_like(q)
-        else:
-            _need(o, "o", q.shape, (torch.bfloat16,), q.device)
-        if lse is None and want_lse:
+    if stream is not None:
+        with _on(stream):
+            return attn_decode_kv4(q, pool, table, seqlens, o, lse, scale, None, want_lse)
+    dev, bf16 = _device_of(q, "q"), torch.bfloat16
+    if q.dim() != 4 or not _is(q, q.shape, bf16, dev):
+        _need(q, "q", (None,) * 4, (bf16,))
+    B, Sq, Hq, d = shape = q.shape
+    n_pages, Hkv, page, max_pages = _kv4(pool, table, seqlens, B, None, d, dev)
+    if o is None:
+        o = torch.empty_like(q)
+    elif not _is(o, shape, bf16, dev):
+        _need(o, "o", shape, (bf16,), q.device)
+    if lse is None:
+        if want_lse:
             lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-        elif lse is not None:
-            _need(lse, "lse", (B, Hq, Sq), (torch.float32,), q.device)
-        n = L.attn_decode_kv4_workspace(B, Sq, Hq, Hkv, d, page, max_pages)
-        work = torch.empty(n, dtype=torch.uint8, device=q.device) if n > 0 else None
-        _check(L.attn_decode_kv4(q.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
-                                 None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(),
-                                 max(n, 0), B, Sq, Hq, Hkv, d, n_pages, page, max_pages, float(scale),
-                                 _stream_ptr(stream)))
+    elif not _is(lse, (B, Hq, Sq), torch.float32, dev):
+        _need(lse, "lse", (B, Hq, Sq), (torch.float32,), q.device)
+    n = _decode_kv4_workspace(B, Sq, Hq, Hkv, d, page, max_pages)
+    work = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    rc = lib().attn_decode_kv4(q.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
+                               None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(), n,
+                               B, Sq, Hq, Hkv, d, n_pages, page, max_pages,
+                               1.0 / math.sqrt(d) if scale is None else float(scale), _stream_here(dev))
+    if rc:
+        _check(rc)
     return o, lse
 
 
@@ -518,21 +583,28 @@ def copy_pages(pool, src, dst, stream=None):
     """Copy pages src[i] of a pool to pages dst[i].  pool: a contiguous CUDA tensor of
     equal pages along its first dimension; src, dst: host int arrays.  A source may
     repeat; no page may be a destination twice, or source and destination.  Returns pool."""
-    if not getattr(pool, "is_cuda", False) or pool.dim() < 1 or not len(pool):
-        raise ValueError("pool must be a CUDA tensor of at least one page")
-    _need(pool, "pool", (None,) * pool.dim(), (pool.dtype,))
+    if stream is not None:
+        with _on(stream):
+            return copy_pages(pool, src, dst)
+    dev = _device_of(pool, "pool")
+    if not pool.numel() or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous tensor of at least one page")
+    n_pages = len(pool)
     src, dst = np.asarray(src), np.asarray(dst)
     if src.ndim != 1 or src.shape != dst.shape:
         raise ValueError(f"src and dst must be vectors of one length, got {src.shape} and {dst.shape}")
-    if len(src) and not (np.issubdtype(src.dtype, np.integer) and np.issubdtype(dst.dtype, np.integer)):
-        raise ValueError(f"src and dst must hold integers, got {src.dtype} and {dst.dtype}")
+    n = len(src)
     for name, x in (("src", src), ("dst", dst)):
-        if x.dtype != np.int32 and len(x) and (x.min() < 0 or x.max() >= len(pool)):
-            raise ValueError(f"{name} names a page outside the pool of {len(pool)} pages")
-    src, dst = np.ascontiguousarray(src, dtype=np.int32), np.ascontiguousarray(dst, dtype=np.int32)
-    with _on(stream):
-        _check(lib().attn_copy_pages(pool.data_ptr(), pool.numel() // len(pool) * pool.element_size(), len(pool),
-                                     _np_ptr(src), _np_ptr(dst), len(src), _stream_ptr(stream)))
+        if n and x.dtype != np.int32:
+            if not np.issubdtype(x.dtype, np.integer):
+                raise ValueError(f"{name} must hold integers, got {x.dtype}")
+            if x.min() < 0 or x.max() >= n_pages:
+                raise ValueError(f"{name} names a page outside the pool of {n_pages} pages")
+    rc = lib().attn_copy_pages(pool.data_ptr(), pool.numel() // n_pages * pool.element_size(), n_pages,
+                               src.astype(np.int32, copy=False).tobytes(), dst.astype(np.int32, copy=False).tobytes(),
+                               n, _stream_here(dev))
+    if rc:
+        _check(rc)
     return pool
 
 

@@ -79,6 +79,8 @@ def default_rope(q, k, positions, axes, freq, interleaved, inverse):
 def _rows(x):
     """x, or a contiguous copy where its layout is not one that eio.rope reads (expanded
     gradients, transposed heads, strides that are not whole 16 bytes)."""
+    if x.is_contiguous() and x.data_ptr() % 16 == 0:
+        return x
     B, N, H, d = x.shape
     e = x.element_size()
     sb, sn, sh, sd = x.stride()
@@ -103,11 +105,16 @@ def _rope_function():
         @staticmethod
         def backward(ctx, dq, dk):
             positions, = ctx.saved_tensors
-            rest = (positions, *ctx.table, not ctx.inverse, ctx.call)
+
+            def back(x, y):
+                if torch.is_grad_enabled():  # a gradient of the gradient is wanted
+                    return _Rope.apply(x, y, positions, *ctx.table, not ctx.inverse, ctx.call)
+                return ctx.call(_rows(x), None if y is None else _rows(y), positions, *ctx.table, not ctx.inverse)
+
             if dq is None:  # only k's output was used
-                gq, gk = None, (None if dk is None else _Rope.apply(dk, None, *rest)[0])
+                gq, gk = None, (None if dk is None else back(dk, None)[0])
             else:
-                gq, gk = _Rope.apply(dq, dk, *rest)
+                gq, gk = back(dq, dk)
             return gq, gk, None, None, None, None, None, None
 
     return _Rope

@@ -67,15 +67,29 @@ __device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t m) {
 
 // Codes are 8 + floor(x / s + 1/2): x / s has a distance of 0 or at least 2^-9
 // from every half-integer (quotients of two 8-bit significands of magnitude at
-// most 7), so x * (1 / s) + 2^-14 rounded to the nearest integer is that floor
-// whatever the last bits of the product.  The addition of 1.5 * 2^23 + 8 rounds
-// and leaves 8 + the integer in the low bits.  Codes stay in 1..15: |x| is at most m
-// and s at least (m / 7) (1 - 2^-8).  inv is 0 for scales 0 and NaN: code 8.
+// most 7: |2 X 2^c - (2 k + 1) S| / 2 S with integers where c >= -1, and below
+// that x / s < 1/2 by at least 2^-9).  So x * (1 / s) + 8.5 + M, rounded to a
+// multiple of 2^-10 or finer by the size of M, has that integer before the point
+// whatever the last bits of the product, ties upwards among them: with M = 1.5 *
+// 2^(23 - i) it is bits i .. i + 3 of the sum.  Codes stay in 1..15: |x| is at most m
+// and s at least (m / 7) (1 - 2^-8).
 __device__ __forceinline__ float kv4_inverse(uint32_t scale_bits) {
-  return scale_bits == 0u || scale_bits >= 0x7f80u ? 0.f : 1.f / __uint_as_float(scale_bits << 16);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__uint_as_float(scale_bits << 16)));
+  return y;
 }
-__device__ __forceinline__ uint32_t kv4_code(float x, float inv) {
-  return __float_as_uint(fmaf(x, inv, 6.103515625e-05f) + 12582920.f) & 15u;
+
+// The codes of eight bf16 values (pairs, low half first), low nibbles first; scale and inverse of their group.
+__device__ __forceinline__ uint32_t kv4_codes(const uint32_t* w, uint32_t scale_bits, float inv) {
+  auto sum = [&](int j, float m) {
+    const uint32_t x = j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16;
+    return __float_as_uint(fmaf(__uint_as_float(x), inv, m));
+  };
+  // three codes at a time at bits 10, 14 and 18
+  auto three = [&](int j) { return (sum(j, 12296.5f) & 0x3c00u) | (sum(j + 1, 776.5f) & 0x3c000u) | (sum(j + 2, 56.5f) & 0x3c0000u); };
+  const uint32_t two = (sum(6, 12296.5f) & 0x3c00u) | (sum(7, 776.5f) & 0x3c000u);
+  const uint32_t c = three(0) >> 10 | three(3) << 2 | two << 14;
+  return scale_bits == 0u || scale_bits >= 0x7f80u ? 0x88888888u : c;
 }
 
 }  // namespace eio

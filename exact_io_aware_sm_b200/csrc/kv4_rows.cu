@@ -13,7 +13,7 @@
 // is written in part, never read.
 //
 // Both are memory bound: per token and head 4 d bytes of bf16 rows and d + d / 8
-// bytes of cache, with about five instructions a value to narrow and two and a half
+// bytes of cache, with about four instructions a value to narrow and two and a half
 // to widen.
 #include <cuda_bf16.h>
 
@@ -72,15 +72,7 @@ __device__ __forceinline__ uint32_t narrow(const uint4& x, uint32_t* scale) {
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   *scale = kv4_scale_bits(m);
-  const float inv = kv4_inverse(*scale);
-  uint32_t out = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // infinities and NaNs have inv 0 and code 8 like the rest of their group
-    const float lo = inv == 0.f ? 0.f : __uint_as_float(w[i] << 16), hi = inv == 0.f ? 0.f : __uint_as_float(w[i] & 0xffff0000u);
-    out |= kv4_code(lo, inv) << (8 * i) | kv4_code(hi, inv) << (8 * i + 4);
-  }
-  return out;
+  return kv4_codes(w, *scale, kv4_inverse(*scale));  // infinities and NaNs have code 8 like the rest of their group
 }
 
 // (c - 8) s of eight codes as bf16, rounded once.

@@ -44,128 +44,122 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return u;
 }
 
-// The 16 channels of eight pairs, as read: two runs of eight, the lo and hi halves of a head or
-// (interleaved) one run of 16.
+// The 16 channels of a piece of work: eight pairs, in 16-byte words that the threads
+// of a head's kChunks pieces read and write side by side.  Word i of piece c is channels
+// V (c + kChunks i) .. + V - 1 with V = 16 / sizeof(T): i < kWords / 2 are in the head's
+// lower half and word i + kWords / 2 holds their partners, or (interleaved) every word its own pairs.
 template <typename T>
 struct Piece {
-  static constexpr int kWords = sizeof(T) / 2;  // uint4 of a run
-  uint4 lo[kWords], hi[kWords];
+  static constexpr int V = 16 / sizeof(T), kWords = 16 / V;
+  uint4 word[kWords];
 };
 
+// Which of a piece's eight pairs pair p of a head is, and of which piece.
+template <typename T, int CHUNKS, bool INTERLEAVED>
+__device__ __forceinline__ int place_of_pair(int p, int* chunk) {
+  constexpr int kPairs = INTERLEAVED ? Piece<T>::V / 2 : Piece<T>::V;  // of a word
+  const int w = p / kPairs;
+  *chunk = w % CHUNKS;
+  return w / CHUNKS * kPairs + p % kPairs;
+}
+
 template <typename T>
-__device__ __forceinline__ void load_piece(const T* lo, const T* hi, Piece<T>& p) {
-#pragma unroll
-  for (int i = 0; i < Piece<T>::kWords; ++i) {
-    p.lo[i] = __ldcs(reinterpret_cast<const uint4*>(lo) + i);
-    p.hi[i] = __ldcs(reinterpret_cast<const uint4*>(hi) + i);
+__device__ __forceinline__ void open_word(const uint4& u, float* f) {
+  if constexpr (sizeof(T) == 2) {
+    unpack8(u, f);
+  } else {
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void open_run(const uint4* u, float* f) {
-  if constexpr (sizeof(T) == 2) {
-    unpack8(u[0], f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f[4 * i] = __uint_as_float(u[i].x), f[4 * i + 1] = __uint_as_float(u[i].y);
-      f[4 * i + 2] = __uint_as_float(u[i].z), f[4 * i + 3] = __uint_as_float(u[i].w);
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_run(T* p, const float* f) {
-  if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = pack8(f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(p + 4 * i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-  }
+__device__ __forceinline__ uint4 close_word(const float* f) {
+  if constexpr (sizeof(T) == 2) return pack8(f);
+  else return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
 template <typename T>
 constexpr int kRopeEach = sizeof(T) == 2 ? 4 : 2;  // pieces of work that a thread has in flight: 128 bytes
 
-struct RopeOffsets {
-  long long q, k, qo, ko;  // of a token's first head
-};
-
 template <typename T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kEach = kRopeEach<T>;
   constexpr int kChunks = D / 16, kHalf = D / 2;  // pieces of eight pairs, pairs of a head
-  // Cosine and sine: two pairs of chunk c at [token][pair / 2 % 4][c], so that the chunks' reads are consecutive.
+  // Cosine and sine: two pairs of piece c at [token][2 of its pairs][c], so that the pieces' reads are consecutive.
   extern __shared__ float4 cs[];
-  RopeOffsets* offs = reinterpret_cast<RopeOffsets*>(cs + a.tokens_per_block * (kHalf / 2));
   const int first = static_cast<int>(blockIdx.x) * a.tokens_per_block;
   const int nt = min(a.tokens_per_block, a.B * a.N - first);
-
-  for (int i = threadIdx.x; i < nt * kHalf; i += kRopeThreads) {
-    const int t = i / kHalf, p = i % kHalf;
-    float s = 0.f, c = 1.f;
-    if (p < a.n_pairs) {
-      const int b = (first + t) / a.N, n = first + t - b * a.N;
-      const long long pos = a.positions[b * a.p_sb + n * a.p_sn + a.axis[p]];
-      const unsigned long long turns = static_cast<unsigned long long>(pos) * a.freq[p];
-      sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-      if (a.inverse) s = -s;
-    }
-    reinterpret_cast<float2*>(cs)[2 * (t * (kHalf / 2) + p % 8 / 2 * kChunks + p / 8) + p % 2] = make_float2(c, s);
-  }
-  if (threadIdx.x < nt) {
-    const int b = (first + threadIdx.x) / a.N, n = first + threadIdx.x - b * a.N;
-    offs[threadIdx.x] = RopeOffsets{b * a.q_sb + n * a.q_sn, b * a.k_sb + n * a.k_sn, b * a.qo_sb + n * a.qo_sn, b * a.ko_sb + n * a.ko_sn};
-  }
-  __syncthreads();
+  const int b0 = first / a.N, n0 = first - b0 * a.N;
 
   const int heads = a.Hq + a.Hk, items = nt * heads * kChunks;
   const int chunk = threadIdx.x % kChunks;  // kRopeThreads is a multiple of kChunks: the same for all of a thread's items
-  const int lo = INTERLEAVED ? 16 * chunk : 8 * chunk, hi = INTERLEAVED ? 16 * chunk + 8 : kHalf + 8 * chunk;
-  for (int i0 = threadIdx.x; i0 < items; i0 += kEach * kRopeThreads) {
-    Piece<T> piece[kEach];
-    T* out[kEach];
-    int tok[kEach];
+  constexpr int V = Piece<T>::V, kWords = Piece<T>::kWords;
+  Piece<T> piece[kEach];
+  T* out[kEach];
+  int tok[kEach];
+  auto load = [&](int i0) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int i = i0 + e * kRopeThreads;
       if (i >= items) break;
       const int row = i / kChunks, t = row / heads, h = row - t * heads;
-      const RopeOffsets& at = offs[t];
       tok[e] = t;
+      int b = b0, n = n0 + t;
+      while (n >= a.N) n -= a.N, ++b;
       const T* in;
       if (h < a.Hq) {
-        in = static_cast<const T*>(a.q) + at.q + h * D;
-        out[e] = static_cast<T*>(a.q_out) + at.qo + h * D;
+        in = static_cast<const T*>(a.q) + b * a.q_sb + n * a.q_sn + h * D;
+        out[e] = static_cast<T*>(a.q_out) + b * a.qo_sb + n * a.qo_sn + h * D;
       } else {
-        in = static_cast<const T*>(a.k) + at.k + (h - a.Hq) * D;
-        out[e] = static_cast<T*>(a.k_out) + at.ko + (h - a.Hq) * D;
+        in = static_cast<const T*>(a.k) + b * a.k_sb + n * a.k_sn + (h - a.Hq) * D;
+        out[e] = static_cast<T*>(a.k_out) + b * a.ko_sb + n * a.ko_sn + (h - a.Hq) * D;
       }
-      load_piece(in + lo, in + hi, piece[e]);
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) piece[e].word[w] = __ldcs(reinterpret_cast<const uint4*>(in + V * (chunk + kChunks * w)));
     }
+  };
+  load(threadIdx.x);  // on its way while the angles are computed
+
+  for (int i = threadIdx.x; i < nt * kHalf; i += kRopeThreads) {
+    const int t = i / kHalf, p = i % kHalf;
+    float s = 0.f, c = 1.f;
+    if (p < a.n_pairs) {
+      int b = b0, n = n0 + t;
+      while (n >= a.N) n -= a.N, ++b;
+      const long long pos = a.positions[b * a.p_sb + n * a.p_sn + a.axis[p]];
+      const unsigned long long turns = static_cast<unsigned long long>(pos) * a.freq[p];
+      sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+      if (a.inverse) s = -s;
+    }
+    int of;
+    const int at = place_of_pair<T, kChunks, INTERLEAVED>(p, &of);
+    reinterpret_cast<float2*>(cs)[2 * (t * (kHalf / 2) + at / 2 * kChunks + of) + at % 2] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  for (int i0 = threadIdx.x; i0 < items; i0 += kEach * kRopeThreads) {
+    if (i0 != threadIdx.x) load(i0);
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       if (i0 + e * kRopeThreads >= items) break;
-      float x[8], y[8];
-      open_run<T>(piece[e].lo, x);
-      open_run<T>(piece[e].hi, y);
-      const float4* w = cs + tok[e] * (kHalf / 2) + chunk;
+      float x[16];
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) open_word<T>(piece[e].word[w], x + V * w);
+      const float4* turn = cs + tok[e] * (kHalf / 2) + chunk;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 r = w[j * kChunks];  // pairs 2 j and 2 j + 1
+        const float4 r = turn[j * kChunks];  // pairs 2 j and 2 j + 1
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float c = k ? r.z : r.x, s = k ? r.w : r.y;
-          const int p = 2 * j + k;
-          float& u = INTERLEAVED ? (p < 4 ? x[(2 * p) & 7] : y[(2 * p) & 7]) : x[p];
-          float& v = INTERLEAVED ? (p < 4 ? x[(2 * p + 1) & 7] : y[(2 * p + 1) & 7]) : y[p];
-          const float u0 = u, v0 = v;
-          u = u0 * c - v0 * s;
-          v = u0 * s + v0 * c;
+          const int p = 2 * j + k, i = INTERLEAVED ? 2 * p : p, partner = INTERLEAVED ? i + 1 : i + 8;
+          const float u = x[i], v = x[partner];
+          x[i] = u * c - v * s;
+          x[partner] = u * s + v * c;
         }
       }
-      store_run(out[e] + lo, x);
-      store_run(out[e] + hi, y);
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) *reinterpret_cast<uint4*>(out[e] + V * (chunk + kChunks * w)) = close_word<T>(x + V * w);
     }
   }
 }
@@ -174,7 +168,7 @@ template <typename T, int D>
 cudaError_t launch_t(bool interleaved, const RopeArgs& a, cudaStream_t s) {
   const int tokens = a.B * a.N;
   const int blocks = (tokens - 1) / a.tokens_per_block + 1;
-  const size_t smem = static_cast<size_t>(a.tokens_per_block) * (D / 2 * sizeof(float2) + sizeof(RopeOffsets));
+  const size_t smem = static_cast<size_t>(a.tokens_per_block) * D / 2 * sizeof(float2);
   if (interleaved) rope_kernel<T, D, true><<<blocks, kRopeThreads, smem, s>>>(a);
   else rope_kernel<T, D, false><<<blocks, kRopeThreads, smem, s>>>(a);
   return cudaGetLastError();
