@@ -44,6 +44,10 @@ namespace eio {
 namespace {
 
 constexpr int kMaxCtas = 148;
+#ifndef KV4_UC
+#define KV4_UC 3
+#endif
+constexpr int kUnitCost = KV4_UC;  // of a unit's start and end, in stages
 constexpr int kRingBudget = 222 * 1024;
 constexpr int kCombineThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -74,11 +78,11 @@ struct Cfg {
   static constexpr int kSlots = W + 2;                 // of a CTA: one a warp, two for what leaves the CTA
 };
 
-// What a unit of len keys is counted for when the runs are cut: its stages and one more for its start and end
-// (the queries' fragments, the results), which cost about as much; nothing where there are no keys.
+// What a unit of len keys is counted for when the runs are cut: its stages and kUnitCost for its start and end (the
+// queries' fragments, the results); nothing where there are no keys.
 template <int KEYS>
 __device__ __forceinline__ int cost_of(int len) {
-  return len > 0 ? (len + KEYS - 1) / KEYS + 1 : 0;
+  return len > 0 ? (len + KEYS - 1) / KEYS + kUnitCost : 0;
 }
 
 // Where the run of a CTA starts: at cost x of all, stage st (of nst) of unit u of sequence b.
@@ -255,11 +259,11 @@ __device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Colum
       const int cost = cost_of<C::kKeys>(ll);
       const long long in = x0 - (end - cost) * units;
       const int u = static_cast<int>(in >> 32 ? in / cost : static_cast<unsigned>(in) / static_cast<unsigned>(cost));
-      nst = cost - 1;
-      st = static_cast<int>(in - static_cast<long long>(u) * cost) - 1;
+      nst = cost - kUnitCost;
+      st = static_cast<int>(in - static_cast<long long>(u) * cost) - kUnitCost;
       if (st < 0) {  // the unit's start, which is no stage
+        left = max(left + st, 0);
         st = 0;
-        --left;
       }
       h = u / cols.blocks;
       cb = u - h * cols.blocks;
@@ -319,7 +323,7 @@ __device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Colum
       fresh = false;
       --left;
       ++st;
-      if (st == nst && left > 0) --left;  // the next unit's start
+      if (st == nst) left = max(left - kUnitCost, 0);  // the next unit's start
       if (st == nst || left == 0) flags |= 2;
       meta[slot] = make_int4(this_b, this_u, k0 | flags, left == 0 ? this_len | static_cast<int>(0x80000000u) : this_len);
       mbar_arrive_expect_tx(&full[slot], (src0 ? bytes0 : 0u) + (src1 ? C::kTile : 0u));
@@ -540,31 +544,34 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
   // The set whose sum a lane's row g + 8 r of psum holds.
   auto set_of_row = [&](int r) { return NS == 4 ? 2 * r + (g >> 2) : NS == 2 ? r : 0; };
 
-  // References that hold the V scales of two tiles (rows of this lane, all finite):
-  // 4 times the largest, so that they seldom move.
-  auto move_refs = [&](const uint32_t (*vs)[2][G / 2]) {
+  // The largest magnitudes of the V scales of two tiles, packed, over all rows.
+  auto largest = [&](const uint32_t (*vs)[2][G / 2], uint32_t* x) {
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) {
+      x[i] = __vmaxu2(__vmaxu2(vs[0][0][i] & 0x7fff7fffu, vs[0][1][i] & 0x7fff7fffu), __vmaxu2(vs[1][0][i] & 0x7fff7fffu, vs[1][1][i] & 0x7fff7fffu));
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) x[i] = __vmaxu2(x[i], __shfl_xor_sync(0xffffffffu, x[i], off));
+    }
+  };
+  // References that hold scales whose largest are x: 4 times those, so that they seldom move.
+  auto move_refs = [&](const uint32_t* x2) {
 #pragma unroll
     for (int grp = 0; grp < G; ++grp) {
-      uint32_t x = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x = max(x, vs[i >> 1][i & 1][grp >> 1] >> (16 * (grp & 1)) & 0x7fffu);
-      }
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, off));
-      const uint32_t old = ref[grp >> 1] >> (16 * (grp & 1)) & 0xffffu;
+      const uint32_t x = x2[grp >> 1] >> (16 * (grp & 1)) & 0xffffu, old = ref[grp >> 1] >> (16 * (grp & 1)) & 0xffffu;
       if (x > old) {
         const int e = min(max(static_cast<int>(x >> 7) + 3, 27), 254);  // biased exponent of the new reference
-        const float down = old == 0 ? 0.f : pow2(max(static_cast<int>(old >> 7) - e, -126));
         const bool own = F == 1 || half == (grp & 1);
+        if (old) {
+          const float down = pow2(max(static_cast<int>(old >> 7) - e, -126));
 #pragma unroll
-        for (int cg = 0; cg < NCG; ++cg)
+          for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (own && set_of_row(i >> 1) == grp / F) psum[cg][i] *= down;
-            acc[cg][grp][0][i] *= down;
-            acc[cg][grp][1][i] *= down;
-          }
+            for (int i = 0; i < 4; ++i) {
+              if (own && set_of_row(i >> 1) == grp / F) psum[cg][i] *= down;
+              acc[cg][grp][0][i] *= down;
+              acc[cg][grp][1][i] *= down;
+            }
+        }
         if (own) rinv[grp / F] = pow2(max(6 + 127 - e, -126));
         const uint32_t bits = static_cast<uint32_t>(e) << 7;
         ref[grp >> 1] = grp & 1 ? (ref[grp >> 1] & 0xffffu) | bits << 16 : (ref[grp >> 1] & 0xffff0000u) | bits;
@@ -616,8 +623,9 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
         for (int i = 0; i < 4; ++i) s[tile][0][i] += __shfl_xor_sync(0xffffffffu, s[tile][0][i], 2);
       }
     }
-    const bool edge = bad || k0 + 32 > ulen - a.Sq + 1;
-    if (edge) {  // some key is past a column's last one, or its page is missing
+    bool moves = __vmaxu2(__vmaxu2(check[0], check[1]), my_ref) != my_ref;
+    if (bad || k0 + 32 > ulen - a.Sq + 1) {  // some key is past a column's last one, or its page is missing
+      moves = false;
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
@@ -627,11 +635,15 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
 #pragma unroll
           for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j) {
               if (gone || key >= vis[cg][j]) s[tile][cg][2 * r + j] = -INFINITY;
+              moves |= mneg[cg][j] == INFINITY;
+            }
 #pragma unroll
-          for (int i = 0; i < G / 2; ++i)
+          for (int i = 0; i < G / 2; ++i) {
             if (gone) vs[tile][r][i] = 0;  // has no weight and moves no reference
+            moves |= __vmaxu2(vs[tile][r][i], ref[i]) != ref[i];
+          }
         }
     }
     // The base and the references move seldom, where weights or scales have grown too large for them: only then are
@@ -645,25 +657,26 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 2; ++j) some[cg][j] = (p[0][cg][j] + p[0][cg][j + 2]) + (p[1][cg][j] + p[1][cg][j + 2]);
     };
-    bool moves = edge || __vmaxu2(__vmaxu2(check[0], check[1]), my_ref) != my_ref;
 #pragma unroll
     for (int cg = 0; cg < NCG; ++cg) {
       weights(cg, mneg[cg][0], mneg[cg][1]);
       moves |= some[cg][0] > kMostWeight || some[cg][1] > kMostWeight;
     }
     if (__any_sync(0xffffffffu, moves)) {
+      uint32_t most[G / 2];
+      largest(vs, most);
       // V scales that are not finite leave the products (0 NaN = NaN would reach other groups' sums, and columns
       // that do not see the key) and go straight to the groups of the columns that see them.
-      uint32_t odd = 0;
+      if (__vmaxu2(most[0], most[G / 2 - 1]) != __vminu2(__vmaxu2(most[0], most[G / 2 - 1]), 0x7f7f7f7fu)) {
+        uint32_t odd = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int i = 0; i < G / 2; ++i) {
-          uint32_t& v = vs[x >> 1][x & 1][i];
-          if ((v & 0x7f80u) == 0x7f80u) odd |= 1u << (x * 8 + 2 * i), v &= 0xffff0000u;
-          if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (x * 8 + 2 * i), v &= 0xffffu;
-        }
-      if (__any_sync(0xffffffffu, odd != 0)) {
+          for (int i = 0; i < G / 2; ++i) {
+            uint32_t& v = vs[x >> 1][x & 1][i];
+            if ((v & 0x7f80u) == 0x7f80u) odd |= 1u << (x * 8 + 2 * i), v &= 0xffff0000u;
+            if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (x * 8 + 2 * i), v &= 0xffffu;
+          }
 #pragma unroll
         for (int cg = 0; cg < NCG; ++cg)
 #pragma unroll
@@ -680,8 +693,9 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
                 for (int i = 0; i < 2; ++i) acc[cg][grp][i][j] = acc[cg][grp][i][j + 2] = __uint_as_float(0x7fffffffu);
               }
           }
+        largest(vs, most);
       }
-      move_refs(vs);
+      move_refs(most);
 #pragma unroll
       for (int cg = 0; cg < NCG; ++cg) {
 #pragma unroll
@@ -692,17 +706,19 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
           v *= fac[cg][j];
           if (v > -mneg[cg][j]) {
-            const float alpha = wm_ex2(-mneg[cg][j] - v);
-            l[cg][j] *= alpha;
+            if (mneg[cg][j] != INFINITY) {
+              const float alpha = wm_ex2(-mneg[cg][j] - v);
+              l[cg][j] *= alpha;
 #pragma unroll
-            for (int grp = 0; grp < G; ++grp)
+              for (int grp = 0; grp < G; ++grp)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                acc[cg][grp][i][j] *= alpha;
-                acc[cg][grp][i][j + 2] *= alpha;
-              }
-            psum[cg][j] *= alpha;
-            psum[cg][j + 2] *= alpha;
+                for (int i = 0; i < 2; ++i) {
+                  acc[cg][grp][i][j] *= alpha;
+                  acc[cg][grp][i][j + 2] *= alpha;
+                }
+              psum[cg][j] *= alpha;
+              psum[cg][j + 2] *= alpha;
+            }
             mneg[cg][j] = -v;
           }
         }
@@ -915,7 +931,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(con
   if (run.x >= total || run.st == 0 || first < before) return;
   // It has parts in CTA i - 1 and in every later one that starts inside it.
   const int n = 1 + __syncthreads_count(tid + i < ctas && runs[min(tid + i, ctas)].x < first + run.nst);
-  const int late = before + 1 < first ? 1 : 0;  // the unit starts after CTA i - 1's run does
+  const int late = before + kUnitCost < first ? 1 : 0;  // the unit starts after CTA i - 1's run does
   const int heads = a.Hq / a.pages.Hkv, live_cols = heads * a.Sq;
   const int uh = run.u / cols.blocks, c0 = (run.u - uh * cols.blocks) * cols.per;
   const int items = cols.per * (D / 4), rows = kCombineThreads / items;
@@ -959,8 +975,11 @@ __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(con
   if (ch == 0 && a.lse) a.lse[(static_cast<size_t>(run.b) * a.Hq + hq) * a.Sq + sq] = sum == 0.f ? -INFINITY : (zero + log2f(sum)) * kLn2;
 }
 
+#ifndef KV4_COLS
+#define KV4_COLS 16
+#endif
 Columns columns_of(int G, int Sq) {
-  const int n = G * Sq, blocks = (n + 15) / 16;
+  const int n = G * Sq, blocks = (n + KV4_COLS - 1) / KV4_COLS;
   return {blocks, (n + blocks - 1) / blocks};
 }
 
