@@ -8,7 +8,7 @@
 // the half-rate integer pipe all matter.
 //
 //   decode_kv4_kernel  persistent, one CTA per SM.  A stage is 32 keys (two
-//     tiles of the cache) of a unit (sequence, KV head, block of at most 8 NCG
+//     tiles of the cache) of a unit (sequence, KV head, block of at most 8
 //     columns, a column being a (query head, token) pair of the head's group).
 //     The stages of all units in a row are cut into equal runs, one for each CTA,
 //     and those into equal runs for its warps: no counters, whatever the lengths.
@@ -44,23 +44,15 @@ namespace eio {
 namespace {
 
 constexpr int kMaxCtas = 148;
-#ifndef KV4_UC
-#define KV4_UC 3
-#endif
-constexpr int kUnitCost = KV4_UC;  // of a unit's start and end, in stages
+constexpr int kUnitCost = 3;  // of a unit's start and end, in stages (measured: 1 to 4)
 constexpr int kRingBudget = 222 * 1024;
 constexpr int kCombineThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kMostWeight = 256.f;  // of a lane's four keys of a column, relative to the base: more moves the base
 
-template <int D, int NCG, int F>
+template <int D, int F>
 struct Cfg {
-#ifndef KV4_WF
-#define KV4_WF 15
-#define KV4_W1 15
-#define KV4_W2 7
-#endif
-  static constexpr int W = F == 2 ? KV4_WF : NCG == 1 ? KV4_W1 : KV4_W2;  // warps that compute; one more brings the stages
+  static constexpr int W = F == 2 || D == 64 ? 15 : 11;  // warps that compute (128 or 168 registers); one more brings the stages
   static constexpr int kKeys = 32;                      // of a stage: two tiles
   static constexpr int kThreads = (W + 1) * 32;
   static constexpr int G = D / 32;
@@ -73,7 +65,7 @@ struct Cfg {
   static constexpr int kOffBars = kOffMeta + W * R * 16;
   static constexpr int kOffSegs = kOffBars + 2 * W * R * 8;  // full and free barriers
   static constexpr int kSmem = kOffSegs + 2 * W * 16 + 16;
-  static constexpr int kCols = 8 * NCG / F;
+  static constexpr int kCols = 8 / F;
   static constexpr int kSlotFloats = kCols * (D + 2);  // numerators [col][D], then (maximum, sum) [col]
   static constexpr int kSlots = W + 2;                 // of a CTA: one a warp, two for what leaves the CTA
 };
@@ -202,10 +194,10 @@ struct Columns {
 };
 
 // The warp that brings the stages: lane i those of warp i's run, into that warp's ring.
-template <int D, int NCG, int F>
+template <int D, int F>
 __device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Columns& cols, Run* runs, uint8_t* ring, int4* meta, uint64_t* full,
                                              uint64_t* free_, int2* first_unit) {
-  using C = Cfg<D, NCG, F>;
+  using C = Cfg<D, F>;
   constexpr int R = C::R, W = C::W;
   const Kv4Pages& pg = a.pages;
   const int lane = threadIdx.x & 31;
@@ -378,10 +370,10 @@ __device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Colum
   __syncwarp();
 }
 
-template <int D, int NCG, int F>
-__global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
+template <int D, int F>
+__global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     decode_kv4_kernel(const DecodeKv4Args a, const Columns cols, Run* runs, float* slots) {
-  using C = Cfg<D, NCG, F>;
+  using C = Cfg<D, F>;
   constexpr int R = C::R, G = C::G, W = C::W;
   extern __shared__ __align__(128) uint8_t smem[];
   const Kv4Pages& pg = a.pages;
@@ -407,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
   __syncthreads();
 
   if (warp == W) {
-    bring_stages<D, NCG, F>(a, cols, runs, ring, meta, full, free_, first_unit);
+    bring_stages<D, F>(a, cols, runs, ring, meta, full, free_, first_unit);
   } else {
     if (warp == W - 1) {  // sequences without a token are shared out among the CTAs
       const int ctas = gridDim.x;
@@ -430,22 +422,22 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
   constexpr int NS = C::N;
   const int half_q = F == 2 ? g >> 2 : 0, half = F == 2 ? t >> 1 : 0;
   const uint32_t pick = half ? 0x3244u : 0x1044u;  // F = 2: this lane's scale of a packed pair, as fp32
-  uint32_t qf[NCG][G][4];         // B fragments of q: two MMAs a group
-  uint32_t less[NCG][2];          // B fragment of -8 sum of q over each group, in four bf16 parts
-  float fac[NCG][2];              // a raw score times this is the score in log2 units
-  int vis[NCG][2];                // keys that the column sees
-  float acc[NCG][G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and + 1: 16 times as large), columns 2 t, 2 t + 1
-  float psum[NCG][4];             // 8 sum of P sv, as rounded: rows g and g + 8 of a tile whose rows 16 / NS n .. are set n's
-  float l[NCG][2];                // sum
-  float mneg[NCG][2];             // less the base (the maximum in log2 units when it last moved); inf: no key was seen yet
-  float rinv[NS];                 // P sv goes in times this: 2^6 over the reference of the lane's group
-  uint32_t ref[G / 2];            // the references as bf16, packed like the scales
-  uint32_t my_ref;                // ref[t % (G / 2)]: the lane checks that word of one row in four lanes' turn
+  uint32_t qf[G][4];         // B fragments of q: two MMAs a group
+  uint32_t less[2];          // B fragment of -8 sum of q over each group, in four bf16 parts
+  float fac[2];              // a raw score times this is the score in log2 units
+  int vis[2];                // keys that the column sees
+  float acc[G][2][4];        // O^T: channels 32 group + 4 g + 2 j (then 16 times the next one, added), columns 2 t, 2 t + 1
+  float psum[4];             // 8 sum of P sv, as rounded: rows g and g + 8 of a tile whose rows 16 / NS n .. are set n's
+  float l[2];                // sum
+  float mneg[2];             // less the base (the maximum in log2 units when it last moved); inf: no key was seen yet
+  float rinv[NS];            // P sv goes in times this: 2^6 over the reference of the lane's group
+  uint32_t ref[G / 2];       // the references as bf16, packed like the scales
+  uint32_t my_ref;           // ref[t % (G / 2)]: the word that the lane checks, of row g + 8 (t / 2)
   int seg_k0 = 0, which = 0;
 
   // The token and the query head (of the KV head's group) of a column; false where there is none.
-  auto column = [&](int cg, int pc, int c0, int* hd, int* tk) {
-    const int c = (cg * 8 + pc) & (C::kCols - 1), col = c0 + c;
+  auto column = [&](int pc, int c0, int* hd, int* tk) {
+    const int c = pc & (C::kCols - 1), col = c0 + c;
     *hd = a.Sq == 1 ? col : col / a.Sq;
     *tk = col - *hd * a.Sq;
     return c < cols.per && col < live_cols;
@@ -453,80 +445,74 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
   auto begin_unit = [&](int ub, int uu, int ulen) {
     const int uh = cols.blocks == 1 ? uu : uu / cols.blocks, c0 = (uu - uh * cols.blocks) * cols.per;
     const size_t row0 = static_cast<size_t>(ub) * a.Sq * a.Hq + uh * heads;
-    uint4 raw[NCG][G];
+    uint4 raw[G];
+    int hd, tk;
+    const bool live = column(g, c0, &hd, &tk);
+    const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) + (row0 + (live ? tk * a.Hq + hd : 0)) * D + 8 * t;
 #pragma unroll
-    for (int cg = 0; cg < NCG; ++cg) {
-      int hd, tk;
-      const bool live = column(cg, g, c0, &hd, &tk);
-      const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) + (row0 + (live ? tk * a.Hq + hd : 0)) * D + 8 * t;
+    for (int grp = 0; grp < G; ++grp) raw[grp] = live ? *reinterpret_cast<const uint4*>(row + 32 * grp) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t mx = 0;
 #pragma unroll
-      for (int grp = 0; grp < G; ++grp) raw[cg][grp] = live ? *reinterpret_cast<const uint4*>(row + 32 * grp) : make_uint4(0u, 0u, 0u, 0u);
+    for (int grp = 0; grp < G; ++grp) {
+      const uint4 w = raw[grp];
+      mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+    }
+    mx = max(mx & 0xffffu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int e = min(max(141 - static_cast<int>(mx >> 7), -100), 100);  // q 2^e
+    const float fc = a.scale_log2 * pow2(24 - e);
+    // Codes n and n + 4 of a word sit 16 bits apart; odd n are masked 4 bits higher, 16 times as large.
+    const uint32_t up = static_cast<uint32_t>(127 + e) << 7 | static_cast<uint32_t>(123 + e) << 23;  // bf16 2^e, 2^(e - 4)
+    float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+    for (int grp = 0; grp < G; ++grp) {
+      const uint32_t y[4] = {times(raw[grp].x, up), times(raw[grp].y, up), times(raw[grp].z, up), times(raw[grp].w, up)};
+      const bool mine = F == 1 || half_q == (grp & 1);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint32_t v = __byte_perm(y[n >> 1], y[2 + (n >> 1)], n & 1 ? 0x7632 : 0x5410);
+        qf[grp][n] = mine ? pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)) : 0u;
+      }
+      // 8 sum q of the columns, by an MMA; -8 sum q of this lane's column g in the two groups of its k
+      const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00800080u, 0x00800080u};
+      float d[4];
+      mma_f16_first(d, eights, qf[grp][0], qf[grp][1]);
+      mma_f16(d, eights, qf[grp][2], qf[grp][3]);
+      const int pc = F == 2 ? (g & 3) + 4 * (grp & 1) : g;
+      const float d0 = __shfl_sync(0xffffffffu, d[0], pc >> 1), d1 = __shfl_sync(0xffffffffu, d[1], pc >> 1);
+      const float sum = pc & 1 ? -d1 : -d0;
+      if (G == 2 || (grp >> 1) == (t & 1)) {
+        if (grp & 1) x1 = sum;
+        else x0 = sum;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[grp][0][i] = acc[grp][1][i] = psum[i] = 0.f;
+    }
+    // Row k of this operand is part k / G of group k % G (d = 128: parts 0 and 1 in b0, 2 and 3 in b1;
+    // d = 64: 0 to 3 in b0), so that a row of K's scales, repeated, is the other operand.
+    uint32_t parts[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      parts[i] = half_q ? 0u : wm_pack_bf16x2(x0, x1);
+      x0 -= __uint_as_float(parts[i] << 16);
+      x1 -= __uint_as_float(parts[i] & 0xffff0000u);
+    }
+    if constexpr (G == 4) {
+      less[0] = t < 2 ? parts[0] : parts[1];
+      less[1] = t < 2 ? parts[2] : parts[3];
+    } else {
+      less[0] = t == 0 ? parts[0] : t == 1 ? parts[1] : t == 2 ? parts[2] : parts[3];
+      less[1] = 0;
     }
 #pragma unroll
-    for (int cg = 0; cg < NCG; ++cg) {
-      uint32_t mx = 0;
-#pragma unroll
-      for (int grp = 0; grp < G; ++grp) {
-        const uint4 w = raw[cg][grp];
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-      }
-      mx = max(mx & 0xffffu, mx >> 16);
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = min(max(141 - static_cast<int>(mx >> 7), -100), 100);  // q 2^e
-      const float fc = a.scale_log2 * pow2(24 - e);
-      // Codes n and n + 4 of a word sit 16 bits apart; odd n are masked 4 bits higher, 16 times as large.
-      const uint32_t up = static_cast<uint32_t>(127 + e) << 7 | static_cast<uint32_t>(123 + e) << 23;  // bf16 2^e, 2^(e - 4)
-      float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-      for (int grp = 0; grp < G; ++grp) {
-        const uint32_t y[4] = {times(raw[cg][grp].x, up), times(raw[cg][grp].y, up), times(raw[cg][grp].z, up), times(raw[cg][grp].w, up)};
-        const bool mine = F == 1 || half_q == (grp & 1);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t v = __byte_perm(y[n >> 1], y[2 + (n >> 1)], n & 1 ? 0x7632 : 0x5410);
-          qf[cg][grp][n] = mine ? pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)) : 0u;
-        }
-        // 8 sum q of the columns, by an MMA; -8 sum q of this lane's column g in the two groups of its k
-        const uint32_t eights[4] = {0x00080008u, 0x00080008u, 0x00800080u, 0x00800080u};
-        float d[4];
-        mma_f16_first(d, eights, qf[cg][grp][0], qf[cg][grp][1]);
-        mma_f16(d, eights, qf[cg][grp][2], qf[cg][grp][3]);
-        const int pc = F == 2 ? (g & 3) + 4 * (grp & 1) : g;
-        const float d0 = __shfl_sync(0xffffffffu, d[0], pc >> 1), d1 = __shfl_sync(0xffffffffu, d[1], pc >> 1);
-        const float sum = pc & 1 ? -d1 : -d0;
-        if (G == 2 || (grp >> 1) == (t & 1)) {
-          if (grp & 1) x1 = sum;
-          else x0 = sum;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[cg][grp][0][i] = acc[cg][grp][1][i] = psum[cg][i] = 0.f;
-      }
-      // Row k of this operand is part k / G of group k % G (d = 128: parts 0 and 1 in b0, 2 and 3 in b1;
-      // d = 64: 0 to 3 in b0), so that a row of K's scales, repeated, is the other operand.
-      uint32_t parts[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        parts[i] = half_q ? 0u : wm_pack_bf16x2(x0, x1);
-        x0 -= __uint_as_float(parts[i] << 16);
-        x1 -= __uint_as_float(parts[i] & 0xffff0000u);
-      }
-      if constexpr (G == 4) {
-        less[cg][0] = t < 2 ? parts[0] : parts[1];
-        less[cg][1] = t < 2 ? parts[2] : parts[3];
-      } else {
-        less[cg][0] = t == 0 ? parts[0] : t == 1 ? parts[1] : t == 2 ? parts[2] : parts[3];
-        less[cg][1] = 0;
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        fac[cg][j] = __shfl_sync(0xffffffffu, fc, (2 * t + j) * 4);
-        int hd, tk;
-        column(cg, 2 * t + j, c0, &hd, &tk);
-        vis[cg][j] = ulen - a.Sq + 1 + tk;
-        mneg[cg][j] = INFINITY;
-        l[cg][j] = 0.f;
-      }
+    for (int j = 0; j < 2; ++j) {
+      fac[j] = __shfl_sync(0xffffffffu, fc, (2 * t + j) * 4);
+      int hd, tk;
+      column(2 * t + j, c0, &hd, &tk);
+      vis[j] = ulen - a.Sq + 1 + tk;
+      mneg[j] = INFINITY;
+      l[j] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < G / 2; ++i) ref[i] = 0;
@@ -564,12 +550,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
         if (old) {
           const float down = pow2(max(static_cast<int>(old >> 7) - e, -126));
 #pragma unroll
-          for (int cg = 0; cg < NCG; ++cg)
-#pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (own && set_of_row(i >> 1) == grp / F) psum[cg][i] *= down;
-              acc[cg][grp][0][i] *= down;
-              acc[cg][grp][1][i] *= down;
+              if (own && set_of_row(i >> 1) == grp / F) psum[i] *= down;
+              acc[grp][0][i] *= down;
+              acc[grp][1][i] *= down;
             }
         }
         if (own) rinv[grp / F] = pow2(max(6 + 127 - e, -126));
@@ -582,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
 
   // Two tiles of a stage: keys k0 .. k0 + 31; bit i of bad: the page of tile i is missing.
   auto two_tiles = [&](const uint8_t* base, int k0, int bad, int ulen) {
-    float s[2][NCG][4];
+    float s[2][4];
     uint32_t vs[2][2][G / 2], check[2];
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
@@ -598,29 +582,25 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
       const uint32_t hi = *reinterpret_cast<const uint32_t*>(p + kv4_off_ks(D) + (g + 8) * (2 * G) + (t % (G / 2)) * 4);
       const uint32_t sc[4] = {lo, hi, lo, hi};
       check[tile] = *reinterpret_cast<const uint32_t*>(p + kv4_off_vs(D) + (g + 8 * (t >> 1)) * (2 * G) + (t % (G / 2)) * 4);
-#pragma unroll
-      for (int cg = 0; cg < NCG; ++cg) mma_bf16_first(s[tile][cg], sc, less[cg][0], less[cg][1]);
-      float raw[NCG][4];
+      mma_bf16_first(s[tile], sc, less[0], less[1]);
+      float raw[4];
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) {
         const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[1][grp] & 0x000f000fu, w[0][grp] & 0x00f000f0u, w[1][grp] & 0x00f000f0u};
         const uint32_t v0 = high_bytes(w[0][grp]), v1 = high_bytes(w[1][grp]), l0 = v0 & 0x000f000fu, l1 = v1 & 0x000f000fu;
         const uint32_t f1[4] = {l0, l1, less_f16x2(v0, l0), less_f16x2(v1, l1)};
         const float k_lo = scale_at(ks[0], grp / F), k_hi = scale_at(ks[1], grp / F);
+        if (grp % F == 0) mma_f16_first(raw, f0, qf[grp][0], qf[grp][1]);
+        else mma_f16(raw, f0, qf[grp][0], qf[grp][1]);
+        mma_f16(raw, f1, qf[grp][2], qf[grp][3]);
+        if (grp % F == F - 1) {
 #pragma unroll
-        for (int cg = 0; cg < NCG; ++cg) {
-          if (grp % F == 0) mma_f16_first(raw[cg], f0, qf[cg][grp][0], qf[cg][grp][1]);
-          else mma_f16(raw[cg], f0, qf[cg][grp][0], qf[cg][grp][1]);
-          mma_f16(raw[cg], f1, qf[cg][grp][2], qf[cg][grp][3]);
-          if (grp % F == F - 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[tile][cg][i] = fmaf(raw[cg][i], i < 2 ? k_lo : k_hi, s[tile][cg][i]);
-          }
+          for (int i = 0; i < 4; ++i) s[tile][i] = fmaf(raw[i], i < 2 ? k_lo : k_hi, s[tile][i]);
         }
       }
       if constexpr (F == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[tile][0][i] += __shfl_xor_sync(0xffffffffu, s[tile][0][i], 2);
+        for (int i = 0; i < 4; ++i) s[tile][i] += __shfl_xor_sync(0xffffffffu, s[tile][i], 2);
       }
     }
     bool moves = __vmaxu2(__vmaxu2(check[0], check[1]), my_ref) != my_ref;
@@ -633,12 +613,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
           const int key = k0 + tile * 16 + 8 * r + g;
           const bool gone = (bad >> tile & 1) || key >= ulen;
 #pragma unroll
-          for (int cg = 0; cg < NCG; ++cg)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (gone || key >= vis[cg][j]) s[tile][cg][2 * r + j] = -INFINITY;
-              moves |= mneg[cg][j] == INFINITY;
-            }
+          for (int j = 0; j < 2; ++j) {
+            if (gone || key >= vis[j]) s[tile][2 * r + j] = -INFINITY;
+            moves |= mneg[j] == INFINITY;
+          }
 #pragma unroll
           for (int i = 0; i < G / 2; ++i) {
             if (gone) vs[tile][r][i] = 0;  // has no weight and moves no reference
@@ -648,20 +626,17 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
     }
     // The base and the references move seldom, where weights or scales have grown too large for them: only then are
     // the column's maximum and the largest scales looked for.
-    float p[2][NCG][4], some[NCG][2];
-    auto weights = [&](int cg, float n0, float n1) {
+    float p[2][4], some[2];
+    auto weights = [&](float n0, float n1) {
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[tile][cg][i] = wm_ex2(fmaf(s[tile][cg][i], fac[cg][i & 1], i & 1 ? n1 : n0));
+        for (int i = 0; i < 4; ++i) p[tile][i] = wm_ex2(fmaf(s[tile][i], fac[i & 1], i & 1 ? n1 : n0));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) some[cg][j] = (p[0][cg][j] + p[0][cg][j + 2]) + (p[1][cg][j] + p[1][cg][j + 2]);
+      for (int j = 0; j < 2; ++j) some[j] = (p[0][j] + p[0][j + 2]) + (p[1][j] + p[1][j + 2]);
     };
-#pragma unroll
-    for (int cg = 0; cg < NCG; ++cg) {
-      weights(cg, mneg[cg][0], mneg[cg][1]);
-      moves |= some[cg][0] > kMostWeight || some[cg][1] > kMostWeight;
-    }
+    weights(mneg[0], mneg[1]);
+    moves |= some[0] > kMostWeight || some[1] > kMostWeight;
     if (__any_sync(0xffffffffu, moves)) {
       uint32_t most[G / 2];
       largest(vs, most);
@@ -678,58 +653,51 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
             if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (x * 8 + 2 * i), v &= 0xffffu;
           }
 #pragma unroll
-        for (int cg = 0; cg < NCG; ++cg)
+        for (int j = 0; j < 2; ++j) {
+          uint32_t sees = 0;
+          for (int x = 0; x < 4; ++x)
+            if (k0 + x * 8 + g < vis[j]) sees |= odd >> (x * 8);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t sees = 0;
-            for (int x = 0; x < 4; ++x)
-              if (k0 + x * 8 + g < vis[cg][j]) sees |= odd >> (x * 8);
+          for (int off = 4; off < 32; off <<= 1) sees |= __shfl_xor_sync(0xffffffffu, sees, off);
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) sees |= __shfl_xor_sync(0xffffffffu, sees, off);
+          for (int grp = 0; grp < G; ++grp)
+            if (sees >> grp & 1) {
 #pragma unroll
-            for (int grp = 0; grp < G; ++grp)
-              if (sees >> grp & 1) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) acc[cg][grp][i][j] = acc[cg][grp][i][j + 2] = __uint_as_float(0x7fffffffu);
-              }
-          }
+              for (int i = 0; i < 2; ++i) acc[grp][i][j] = acc[grp][i][j + 2] = __uint_as_float(0x7fffffffu);
+            }
+        }
         largest(vs, most);
       }
       move_refs(most);
 #pragma unroll
-      for (int cg = 0; cg < NCG; ++cg) {
+      for (int j = 0; j < 2; ++j) {
+        float v = fmaxf(fmaxf(s[0][j], s[0][j + 2]), fmaxf(s[1][j], s[1][j + 2]));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        v *= fac[j];
+        if (v > -mneg[j]) {
+          if (mneg[j] != INFINITY) {
+            const float alpha = wm_ex2(-mneg[j] - v);
+            l[j] *= alpha;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v = fmaxf(fmaxf(s[0][cg][j], s[0][cg][j + 2]), fmaxf(s[1][cg][j], s[1][cg][j + 2]));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          v *= fac[cg][j];
-          if (v > -mneg[cg][j]) {
-            if (mneg[cg][j] != INFINITY) {
-              const float alpha = wm_ex2(-mneg[cg][j] - v);
-              l[cg][j] *= alpha;
+            for (int grp = 0; grp < G; ++grp)
 #pragma unroll
-              for (int grp = 0; grp < G; ++grp)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  acc[cg][grp][i][j] *= alpha;
-                  acc[cg][grp][i][j + 2] *= alpha;
-                }
-              psum[cg][j] *= alpha;
-              psum[cg][j + 2] *= alpha;
-            }
-            mneg[cg][j] = -v;
+              for (int i = 0; i < 2; ++i) {
+                acc[grp][i][j] *= alpha;
+                acc[grp][i][j + 2] *= alpha;
+              }
+            psum[j] *= alpha;
+            psum[j + 2] *= alpha;
           }
+          mneg[j] = -v;
         }
-        // a column that still sees no key has weights 0
-        weights(cg, mneg[cg][0] == INFINITY ? 0.f : mneg[cg][0], mneg[cg][1] == INFINITY ? 0.f : mneg[cg][1]);
       }
+      // a column that still sees no key has weights 0
+      weights(mneg[0] == INFINITY ? 0.f : mneg[0], mneg[1] == INFINITY ? 0.f : mneg[1]);
     }
 #pragma unroll
-    for (int cg = 0; cg < NCG; ++cg)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) l[cg][j] += some[cg][j];
+    for (int j = 0; j < 2; ++j) l[j] += some[j];
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       const uint8_t* at = base + tile * C::kTile;
@@ -741,24 +709,17 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
         const float v_lo = scale_at(vs[tile][0], n) * rinv[n], v_hi = scale_at(vs[tile][1], n) * rinv[n];
         const uint32_t e0 = set_of_row(0) == n ? 0x00080008u : 0u, e1 = set_of_row(1) == n ? 0x00080008u : 0u;
         const uint32_t eights[4] = {e0, e1, e0, e1};
-        uint32_t b0[NCG], b1[NCG];
-#pragma unroll
-        for (int cg = 0; cg < NCG; ++cg) {
-          b0[cg] = transposed(pack_f16x2(p[tile][cg][0] * v_lo, p[tile][cg][1] * v_lo));
-          b1[cg] = transposed(pack_f16x2(p[tile][cg][2] * v_hi, p[tile][cg][3] * v_hi));
-          mma_f16(psum[cg], eights, b0[cg], b1[cg]);
-        }
+        const uint32_t b0 = transposed(pack_f16x2(p[tile][0] * v_lo, p[tile][1] * v_lo));
+        const uint32_t b1 = transposed(pack_f16x2(p[tile][2] * v_hi, p[tile][3] * v_hi));
+        mma_f16(psum, eights, b0, b1);
 #pragma unroll
         for (int grp = n * F; grp < n * F + F; ++grp) {
           // rows g + 8 take both codes of a byte, c + 16 c': the rows g are taken off them at the end
           const uint32_t v0 = high_bytes(w[0][grp]), v1 = high_bytes(w[1][grp]);
           const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[0][grp] & 0x00ff00ffu, w[1][grp] & 0x000f000fu, w[1][grp] & 0x00ff00ffu};
           const uint32_t f1[4] = {v0 & 0x000f000fu, v0, v1 & 0x000f000fu, v1};
-#pragma unroll
-          for (int cg = 0; cg < NCG; ++cg) {
-            mma_f16(acc[cg][grp][0], f0, b0[cg], b1[cg]);
-            mma_f16(acc[cg][grp][1], f1, b0[cg], b1[cg]);
-          }
+          mma_f16(acc[grp][0], f0, b0, b1);
+          mma_f16(acc[grp][1], f1, b0, b1);
         }
       }
     }
@@ -771,45 +732,43 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
     const bool whole = starts && ends;
     float* slot = near ? reinterpret_cast<float*>(ring) : my_slots + warp * C::kSlotFloats;
 #pragma unroll
-    for (int cg = 0; cg < NCG; ++cg)
+    for (int j = 0; j < 2; ++j) {
+      float sum = l[j];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      float eight[NS];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float sum = l[cg][j];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        float eight[NS];
+      for (int n = 0; n < NS; ++n) {
+        const float x = psum[(NS == 4 ? n >> 1 : n) * 2 + j];
+        eight[n] = NS == 4 ? __shfl_sync(0xffffffffu, x, 16 * (n & 1) + t) : x;
+      }
+      int hd, tk;
+      if (column(2 * t + j, c0, &hd, &tk)) {
+        const int c = (2 * t + j) & (C::kCols - 1);
+        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (row0 + static_cast<size_t>(tk) * a.Hq + hd) * D + 4 * g + 32 * half;
+        float* part = slot + c * D + 4 * g + 32 * half;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          const float x = psum[cg][(NS == 4 ? n >> 1 : n) * 2 + j];
-          eight[n] = NS == 4 ? __shfl_sync(0xffffffffu, x, 16 * (n & 1) + t) : x;
+          // 1 / rinv, exactly; raw numerators are in units of 2^-24 (odd channels: of 2^-20, their neighbour's taken off)
+          const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv, less8 = eight[n] * pow2(24);
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float(&own)[4] = acc[F * n][i >> 1], (&odd)[4] = acc[F * n + F - 1][i >> 1];
+            const float even = half ? odd[j] : own[j], both = half ? odd[j + 2] : own[j + 2];
+            y[i] = fmaf(i & 1 ? both - even : even, i & 1 ? pow2(20) : pow2(24), -less8) * f;
+          }
+          if (whole) *reinterpret_cast<uint2*>(o + 32 * F * n) = make_uint2(wm_pack_bf16x2(y[0], y[1]), wm_pack_bf16x2(y[2], y[3]));
+          else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);
         }
-        int hd, tk;
-        if (column(cg, 2 * t + j, c0, &hd, &tk)) {
-          const int c = (cg * 8 + 2 * t + j) & (C::kCols - 1);
-          const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (row0 + static_cast<size_t>(tk) * a.Hq + hd) * D + 4 * g + 32 * half;
-          float* part = slot + c * D + 4 * g + 32 * half;
-#pragma unroll
-          for (int n = 0; n < NS; ++n) {
-            // 1 / rinv, exactly; raw numerators are in units of 2^-24 (odd channels: of 2^-20, their neighbour's taken off)
-            const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv, less8 = eight[n] * pow2(24);
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float(&own)[4] = acc[cg][F * n][i >> 1], (&odd)[4] = acc[cg][F * n + F - 1][i >> 1];
-              const float even = half ? odd[j] : own[j], both = half ? odd[j + 2] : own[j + 2];
-              y[i] = fmaf(i & 1 ? both - even : even, i & 1 ? pow2(20) : pow2(24), -less8) * f;
-            }
-            if (whole) *reinterpret_cast<uint2*>(o + 32 * F * n) = make_uint2(wm_pack_bf16x2(y[0], y[1]), wm_pack_bf16x2(y[2], y[3]));
-            else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);
-          }
-          if (g == 0 && half == 0) {
-            if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(-mneg[cg][j], sum);
-            else if (a.lse) a.lse[(static_cast<size_t>(ub) * a.Hq + uh * heads + hd) * a.Sq + tk] = sum == 0.f ? -INFINITY : (log2f(sum) - mneg[cg][j]) * kLn2;
-          }
+        if (g == 0 && half == 0) {
+          if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(-mneg[j], sum);
+          else if (a.lse) a.lse[(static_cast<size_t>(ub) * a.Hq + uh * heads + hd) * a.Sq + tk] = sum == 0.f ? -INFINITY : (log2f(sum) - mneg[j]) * kLn2;
         }
       }
+    }
     __syncwarp();
     if (!whole && lane == 0) segs[2 * warp + which] = Segment{ub, uu, starts | ends << 1, near};
     which = 1;
@@ -915,10 +874,10 @@ __global__ void __launch_bounds__(Cfg<D, NCG, F>::kThreads, 1)
   }
 }
 
-template <int D, int NCG, int F>
+template <int D, int F>
 __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(const DecodeKv4Args a, const Columns cols, int ctas,
                                                                             const Run* runs, const float* slots) {
-  using C = Cfg<D, NCG, F>;
+  using C = Cfg<D, F>;
   __shared__ float4 part_o[kCombineThreads];
   __shared__ float2 part_ml[kCombineThreads];
   const int i = blockIdx.x + 1;  // the boundary before the run of CTA i
@@ -975,11 +934,11 @@ __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(con
   if (ch == 0 && a.lse) a.lse[(static_cast<size_t>(run.b) * a.Hq + hq) * a.Sq + sq] = sum == 0.f ? -INFINITY : (zero + log2f(sum)) * kLn2;
 }
 
-#ifndef KV4_COLS
-#define KV4_COLS 16
-#endif
+// More columns than an MMA has go in equal blocks, which share the cache's bytes through L2: 16 columns in two
+// blocks took 47 us where two MMAs a code fragment took 51 (19 sequences x 4 tokens: the wider state left
+// too few warps).
 Columns columns_of(int G, int Sq) {
-  const int n = G * Sq, blocks = (n + KV4_COLS - 1) / KV4_COLS;
+  const int n = G * Sq, blocks = (n + 7) / 8;
   return {blocks, (n + blocks - 1) / blocks};
 }
 
@@ -992,22 +951,22 @@ int ctas_of(int B, int units, long long max_tokens, int keys) {
   return most < kMaxCtas ? static_cast<int>(most) : kMaxCtas;
 }
 
-template <int D, int NCG, int F>
+template <int D, int F>
 size_t workspace_of(int B, int units, long long max_tokens) {
-  using C = Cfg<D, NCG, F>;
+  using C = Cfg<D, F>;
   return kRunsBytes + static_cast<size_t>(ctas_of(B, units, max_tokens, C::kKeys)) * C::kSlots * C::kSlotFloats * sizeof(float);
 }
 
-template <int D, int NCG, int F>
-cudaError_t launch_dn(const Columns cols, const DecodeKv4Args& a, cudaStream_t s) {
-  using C = Cfg<D, NCG, F>;
+template <int D, int F>
+cudaError_t launch_df(const Columns cols, const DecodeKv4Args& a, cudaStream_t s) {
+  using C = Cfg<D, F>;
   static_assert(C::kSmem <= 227 * 1024 && C::R >= 2 && 2 * C::W <= 32 && C::R * C::kStage >= C::kSlotFloats * 4, "the rings of all warps fit one SM");
   static DeviceOnce attr_set;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!attr_set.test(dev)) {
-    e = cudaFuncSetAttribute(decode_kv4_kernel<D, NCG, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(decode_kv4_kernel<D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set.set(dev);
   }
@@ -1018,38 +977,31 @@ cudaError_t launch_dn(const Columns cols, const DecodeKv4Args& a, cudaStream_t s
   const int grid = most < sms ? most : sms;
   Run* runs = static_cast<Run*>(a.work);
   float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(a.work) + kRunsBytes);
-  decode_kv4_kernel<D, NCG, F><<<grid, C::kThreads, C::kSmem, s>>>(a, cols, runs, slots);
+  decode_kv4_kernel<D, F><<<grid, C::kThreads, C::kSmem, s>>>(a, cols, runs, slots);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_after_pdl(decode_kv4_combine_kernel<D, NCG, F>, dim3(grid - 1), dim3(kCombineThreads), 0, s, a, cols, grid,
+  return launch_after_pdl(decode_kv4_combine_kernel<D, F>, dim3(grid - 1), dim3(kCombineThreads), 0, s, a, cols, grid,
                           static_cast<const Run*>(runs), static_cast<const float*>(slots));
 }
 
-// The columns (query head, token) of a KV head's group decide the form.  Up to 4 fill half an MMA and share it
-// between two groups of channels; up to 8 fill one; up to 16 two.
+// Up to 4 columns fill half an MMA and share it between two groups of channels (F = 2), up to 8 fill one (F = 1).
 template <typename Fn>
 auto with_form(int d, int per, Fn fn) {
   using std::integral_constant;
-  if (d == 64) {
-    if (per <= 4) return fn(integral_constant<int, 64>{}, integral_constant<int, 1>{}, integral_constant<int, 2>{});
-    if (per <= 8) return fn(integral_constant<int, 64>{}, integral_constant<int, 1>{}, integral_constant<int, 1>{});
-    return fn(integral_constant<int, 64>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
-  }
-  if (per <= 4) return fn(integral_constant<int, 128>{}, integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (per <= 8) return fn(integral_constant<int, 128>{}, integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  return fn(integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  if (d == 64) return per <= 4 ? fn(integral_constant<int, 64>{}, integral_constant<int, 2>{}) : fn(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  return per <= 4 ? fn(integral_constant<int, 128>{}, integral_constant<int, 2>{}) : fn(integral_constant<int, 128>{}, integral_constant<int, 1>{});
 }
 
 }  // namespace
 
 size_t decode_kv4_workspace_bytes(int B, int Sq, int Hq, int Hkv, long long max_tokens, int d) {
   const Columns c = columns_of(Hq / Hkv, Sq);
-  return with_form(d, c.per, [&](auto D, auto NCG, auto F) { return workspace_of<D(), NCG(), F()>(B, Hkv * c.blocks, max_tokens); });
+  return with_form(d, c.per, [&](auto D, auto F) { return workspace_of<D(), F()>(B, Hkv * c.blocks, max_tokens); });
 }
 
 cudaError_t launch_decode_kv4(int d, const DecodeKv4Args& a, cudaStream_t s) {
   const Columns c = columns_of(a.Hq / a.pages.Hkv, a.Sq);
-  return with_form(d, c.per, [&](auto D, auto NCG, auto F) { return launch_dn<D(), NCG(), F()>(c, a, s); });
+  return with_form(d, c.per, [&](auto D, auto F) { return launch_df<D(), F()>(c, a, s); });
 }
 
 }  // namespace eio
