@@ -51,6 +51,14 @@ int check_pages(int B, int Hkv, int d, int n_pages, int page, int max_pages, Kv4
   return ATTN_OK;
 }
 
+// Rows that an append or a read covers: a warp each 16 of a head, in a grid of at most 2^31 - 1 blocks.
+int check_rows(int B, int N, int Hkv) {
+  if (N < 1 || static_cast<long long>(B) * N >= (1ll << 31))
+    return fail(ATTN_ERR_SHAPE, "N must be >= 1 and B * N below 2^31");
+  if (static_cast<double>(B) * (N / 16 + 2) * Hkv >= 8589934592.0) return fail(ATTN_ERR_SHAPE, "too many rows");
+  return ATTN_OK;
+}
+
 int ready(void* stream, int** err) {
   if (int rc = require_sm100()) return rc;
   return device_error_word(static_cast<cudaStream_t>(stream), err);
@@ -121,8 +129,7 @@ int attn_kv4_append(const void* k, const void* v, void* pool, const int32_t* tab
     return fail(ATTN_ERR_NULL, "k, v, pool, table, seqlens and strides must be non-NULL");
   Kv4AppendArgs a{};
   if (int rc = check_pages(B, Hkv, d, n_pages, page, max_pages, &a.pages)) return rc;
-  if (N < 1 || static_cast<long long>(B) * N >= (1ll << 31))
-    return fail(ATTN_ERR_SHAPE, "N must be >= 1 and B * N below 2^31");
+  if (int rc = check_rows(B, N, Hkv)) return rc;
   for (int i = 0; i < 4; ++i)
     if (strides[i] < 0 || strides[i] % 8 != 0)
       return fail(ATTN_ERR_ALIGN, "strides of k and v must be multiples of 16 bytes");
@@ -148,8 +155,7 @@ int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, cons
     return fail(ATTN_ERR_NULL, "k, v, pool, table and seqlens must be non-NULL");
   Kv4ReadArgs a{};
   if (int rc = check_pages(B, Hkv, d, n_pages, page, max_pages, &a.pages)) return rc;
-  if (N < 1 || static_cast<long long>(B) * N >= (1ll << 31))
-    return fail(ATTN_ERR_SHAPE, "N must be >= 1 and B * N below 2^31");
+  if (int rc = check_rows(B, N, Hkv)) return rc;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pool, 128) || !aligned(table, 4) || !aligned(seqlens, 4) ||
       !aligned(start, 4))
     return fail(ATTN_ERR_ALIGN, "k and v must be 16-byte aligned, pool 128-byte, table, seqlens and start 4-byte");

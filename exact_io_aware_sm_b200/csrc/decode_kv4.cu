@@ -3,32 +3,46 @@
 //
 //     O = softmax(q K^T scale) V,   K = (ck - 8) sk,  V = (cv - 8) sv
 //
-// The cache is read once: 18 d / 16 bytes a key and KV head, against 1.2
-// instructions a value to widen the codes, so the memory, the issue slots and
-// the half-rate integer pipe all matter.
+// The cache is read once: 18 d / 8 bits of codes and scales a key and KV head.
+// What bounds the kernel beside HBM is the integer pipe, which takes two cycles an
+// instruction: 0.5 of them a value to widen the codes.  524287 keys x 8 KV heads (604
+// MB) take 114 to 123 us, 4.9 to 5.3 TB/s of the 6.46 that a copy reaches; the loads
+// alone (a build without the arithmetic) took 101.
 //
 //   decode_kv4_kernel  persistent, one CTA per SM.  A stage is 32 keys (two
 //     tiles of the cache) of a unit (sequence, KV head, block of at most 8
 //     columns, a column being a (query head, token) pair of the head's group).
-//     The stages of all units in a row are cut into equal runs, one for each CTA,
-//     and those into equal runs for its warps: no counters, whatever the lengths.
-//     Each warp is its own pipeline: a ring of stages filled by bulk copies (a
-//     tile is one contiguous run), an online softmax, warp-level MMAs on the
-//     codes.  The bits of a nibble masked out of a word are the fp16 number
-//     c 2^-24, or c 2^-20 four bits higher: widening two codes costs one AND.
+//     The units in a row, each counted as its stages and three more for its start and
+//     end, are cut into equal runs, one for each CTA, and those into equal runs for
+//     its warps: no counters, whatever the lengths.  One warp brings the stages of
+//     all the others (lane i those of warp i) into a ring for each by bulk copies: a
+//     tile is one contiguous run.  The others never wait for one another: online
+//     softmax and warp-level MMAs on the codes.  The bits of a nibble masked out of a
+//     word are the fp16 number c 2^-24, or c 2^-20 four bits higher, so that widening
+//     two codes costs one AND; fp16's subnormal numbers are exact in the MMA.
 //       S^T (16 keys x 8 columns): two MMAs for each group of 32 channels, whose
-//         scale multiplies their sum; the -8 of c - 8 is the accumulator's first
-//         value (-8 sum q).  q goes in as fp16, scaled by a power of two so that its
-//         largest magnitude is in [2^14, 2^15): exact down to 2^-28 of that.
+//         scale multiplies their sum.  The -8 of c - 8 is one more MMA, of the
+//         scales with -8 sum q over each group in four bf16 parts (32 bits).  q goes
+//         in as fp16, scaled by a power of two so that its largest magnitude is in
+//         [2^14, 2^15): exact down to 2^-28 of that.
 //       O^T (d x 8 columns): the scale belongs to the key, so P sv is rounded to
 //         fp16, relative to a power of two (a reference) at least as large as
-//         every scale of the group so far, as P is relative to the running maximum:
-//         2^-12 of each term, and exact to 2^-28 of the largest.  The -8 is taken
-//         off at the end: one more MMA a group keeps 8 sum P sv of the rounded terms.
+//         every scale of the group so far, as P is relative to a base that is at most 2^8
+//         below the running maximum: 2^-12 of each term down to 2^-28 of the largest.
+//         Odd channels' rows take c + 16 c' (a byte as it is), and the even ones'
+//         are taken off at the end; so is the -8: one more MMA a group sums 8 P sv as
+//         rounded.
+//     The base and the references move only when a weight or a scale has outgrown
+//     them (a test of sums that are taken anyway), so that a stage needs no maximum
+//     and no shuffles (93 -> 82 us for 64 sequences of 1024 to 8192 keys, with what
+//     it made possible).
+//     Up to 4 columns (grouped heads, one token) fill half an MMA; the other half
+//     then holds the odd groups of channels (F = 2): scaling, P sv and the sums cost
+//     half (157 -> 138 us for the 524287 keys).
 //     A unit that lies in one warp's run is finished there, one in a CTA's run by
 //     the CTA once its warps are done; the others leave numerators, maxima and sums.
 //   decode_kv4_combine_kernel  one CTA for each boundary between two runs: joins the
-//     unit that lies across it.
+//     unit that lies across it, in the order of its parts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -409,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         for (; none; none &= none - 1) {
           const size_t be = b0 + (__ffs(none) - 1) * ctas;
           uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + be * a.Sq * a.Hq * D);
-          for (int i = lane; i < a.Sq * a.Hq * (D / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+          for (long long i = lane; i < static_cast<long long>(a.Sq) * a.Hq * (D / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
           if (a.lse)
             for (int i = lane; i < a.Sq * a.Hq; i += 32) a.lse[be * a.Sq * a.Hq + i] = -INFINITY;
         }

@@ -67,7 +67,8 @@ def _read(**kw):
 PAGE_REFUSALS = [
     (1, dict(k=None)), (1, dict(pool=None)), (1, dict(table=None)), (1, dict(lens=None)), (2, dict(B=0)), (2, dict(N=0)),
     (2, dict(H=0)), (2, dict(n_pages=0)), (2, dict(mp=0)), (4, dict(d=32)), (4, dict(page=48)), (4, dict(page=8)),
-    (4, dict(page=512)), (2, dict(mp=1 << 27)), (2, dict(B=1 << 16, N=1 << 15)), (3, dict(k=FAKE + 8)),
+    (4, dict(page=512)), (2, dict(mp=1 << 27)), (2, dict(B=1 << 16, N=1 << 15)), (2, dict(B=1 << 20, N=1, H=1 << 15)), (2, dict(H=1 << 16)),
+    (2, dict(B=(1 << 24) + 1)), (3, dict(k=FAKE + 8)),
     (3, dict(pool=FAKE + 16)), (3, dict(table=FAKE + 2))]
 
 
