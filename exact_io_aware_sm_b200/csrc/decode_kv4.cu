@@ -29,9 +29,10 @@
 //         fp16, relative to a power of two (a reference) at least as large as
 //         every scale of the group so far, as P is relative to a base that is at most 2^8
 //         below the running maximum: 2^-12 of each term down to 2^-28 of the largest.
-//         Odd channels' rows take c + 16 c' (a byte as it is), and the even ones'
-//         are taken off at the end; so is the -8: one more MMA a group sums 8 P sv as
-//         rounded.
+//         The codes go in as c - 8, a subtraction of subnormal numbers for two of
+//         them: taking 8 sum P sv off at the end cost a third less, but over the
+//         524287 keys the sums of c lost the digits that the difference is made of
+//         (O off by 0.0041 of its norm instead of 0.0017).
 //     The base and the references move only when a weight or a scale has outgrown
 //     them (a test of sums that are taken anyway), so that a stage needs no maximum
 //     and no shuffles (93 -> 82 us for 64 sequences of 1024 to 8192 keys, with what
@@ -440,8 +441,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   uint32_t less[2];          // B fragment of -8 sum of q over each group, in four bf16 parts
   float fac[2];              // a raw score times this is the score in log2 units
   int vis[2];                // keys that the column sees
-  float acc[G][2][4];        // O^T: channels 32 group + 4 g + 2 j (then 16 times the next one, added), columns 2 t, 2 t + 1
-  float psum[4];             // 8 sum of P sv, as rounded: rows g and g + 8 of a tile whose rows 16 / NS n .. are set n's
+  float acc[G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and 16 times the next one), columns 2 t, 2 t + 1
   float l[2];                // sum
   float mneg[2];             // less the base (the maximum in log2 units when it last moved); inf: no key was seen yet
   float rinv[NS];            // P sv goes in times this: 2^6 over the reference of the lane's group
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         else x0 = sum;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[grp][0][i] = acc[grp][1][i] = psum[i] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[grp][0][i] = acc[grp][1][i] = 0.f;
     }
     // Row k of this operand is part k / G of group k % G (d = 128: parts 0 and 1 in b0, 2 and 3 in b1;
     // d = 64: 0 to 3 in b0), so that a row of K's scales, repeated, is the other operand.
@@ -541,8 +541,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     else return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
   };
 
-  // The set whose sum a lane's row g + 8 r of psum holds.
-  auto set_of_row = [&](int r) { return NS == 4 ? 2 * r + (g >> 2) : NS == 2 ? r : 0; };
 
   // The largest magnitudes of the V scales of two tiles, packed, over all rows.
   auto largest = [&](const uint32_t (*vs)[2][G / 2], uint32_t* x) {
@@ -565,7 +563,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const float down = pow2(max(static_cast<int>(old >> 7) - e, -126));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (own && set_of_row(i >> 1) == grp / F) psum[i] *= down;
               acc[grp][0][i] *= down;
               acc[grp][1][i] *= down;
             }
@@ -701,8 +698,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
                 acc[grp][i][j] *= alpha;
                 acc[grp][i][j + 2] *= alpha;
               }
-            psum[j] *= alpha;
-            psum[j + 2] *= alpha;
           }
           mneg[j] = -v;
         }
@@ -721,17 +716,16 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         const float v_lo = scale_at(vs[tile][0], n) * rinv[n], v_hi = scale_at(vs[tile][1], n) * rinv[n];
-        const uint32_t e0 = set_of_row(0) == n ? 0x00080008u : 0u, e1 = set_of_row(1) == n ? 0x00080008u : 0u;
-        const uint32_t eights[4] = {e0, e1, e0, e1};
         const uint32_t b0 = transposed(pack_f16x2(p[tile][0] * v_lo, p[tile][1] * v_lo));
         const uint32_t b1 = transposed(pack_f16x2(p[tile][2] * v_hi, p[tile][3] * v_hi));
-        mma_f16(psum, eights, b0, b1);
 #pragma unroll
         for (int grp = n * F; grp < n * F + F; ++grp) {
-          // rows g + 8 take both codes of a byte, c + 16 c': the rows g are taken off them at the end
+          // c - 8 in rows g and 16 (c - 8) in rows g + 8, from c, 16 c, and c + 16 c' with 128 + c: all exact
           const uint32_t v0 = high_bytes(w[0][grp]), v1 = high_bytes(w[1][grp]);
-          const uint32_t f0[4] = {w[0][grp] & 0x000f000fu, w[0][grp] & 0x00ff00ffu, w[1][grp] & 0x000f000fu, w[1][grp] & 0x00ff00ffu};
-          const uint32_t f1[4] = {v0 & 0x000f000fu, v0, v1 & 0x000f000fu, v1};
+          const uint32_t x0 = (v0 & 0x000f000fu) | 0x00800080u, x1 = (v1 & 0x000f000fu) | 0x00800080u;
+          const uint32_t f0[4] = {less_f16x2(w[0][grp] & 0x000f000fu, 0x00080008u), less_f16x2(w[0][grp] & 0x00f000f0u, 0x00800080u),
+                                  less_f16x2(w[1][grp] & 0x000f000fu, 0x00080008u), less_f16x2(w[1][grp] & 0x00f000f0u, 0x00800080u)};
+          const uint32_t f1[4] = {less_f16x2(x0, 0x00880088u), less_f16x2(v0, x0), less_f16x2(x1, 0x00880088u), less_f16x2(v1, x1)};
           mma_f16(acc[grp][0], f0, b0, b1);
           mma_f16(acc[grp][1], f1, b0, b1);
         }
@@ -751,12 +745,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      float eight[NS];
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const float x = psum[(NS == 4 ? n >> 1 : n) * 2 + j];
-        eight[n] = NS == 4 ? __shfl_sync(0xffffffffu, x, 16 * (n & 1) + t) : x;
-      }
       int hd, tk;
       if (column(2 * t + j, c0, &hd, &tk)) {
         const int c = (2 * t + j) & (C::kCols - 1);
@@ -765,14 +753,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         float* part = slot + c * D + 4 * g + 32 * half;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          // 1 / rinv, exactly; raw numerators are in units of 2^-24 (odd channels: of 2^-20, their neighbour's taken off)
-          const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv, less8 = eight[n] * pow2(24);
+          // 1 / rinv, exactly; raw numerators are in units of 2^-24 (odd channels: of 2^-20)
+          const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv;
           float y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float(&own)[4] = acc[F * n][i >> 1], (&odd)[4] = acc[F * n + F - 1][i >> 1];
-            const float even = half ? odd[j] : own[j], both = half ? odd[j + 2] : own[j + 2];
-            y[i] = fmaf(i & 1 ? both - even : even, i & 1 ? pow2(20) : pow2(24), -less8) * f;
+            const int at = j + 2 * (i & 1);
+            y[i] = (half ? acc[F * n + F - 1][i >> 1][at] : acc[F * n][i >> 1][at]) * (i & 1 ? pow2(20) : pow2(24)) * f;
           }
           if (whole) *reinterpret_cast<uint2*>(o + 32 * F * n) = make_uint2(wm_pack_bf16x2(y[0], y[1]), wm_pack_bf16x2(y[2], y[3]));
           else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);

@@ -86,10 +86,10 @@ def rows(pool, pages, page, n, d):
 
 def decode(q, ks, vs, scale):
     """O [B, Sq, Hq, d], LSE [B, Hq, Sq], and the sizes that bound the error of O and of
-    LSE: sum_j p_j |v_j|, the largest sum of |q k| scale of a row, and sum_j p_j max |v_j|
-    over the channel's group of 32.  q [B, Sq, Hq, d]; ks, vs a list of [len, Hkv, d]."""
+    LSE: sum_j p_j |v_j| and the largest sum of |q k| scale of a row.  q [B, Sq, Hq, d];
+    ks, vs a list of [len, Hkv, d]."""
     B, Sq, Hq, d = q.shape
-    o, w, top = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
+    o, w = np.zeros(q.shape), np.zeros(q.shape)
     lse, a = np.full((B, Hq, Sq), -np.inf), np.zeros((B, Hq, Sq))
     for b in range(B):
         n, H = ks[b].shape[:2]
@@ -104,8 +104,7 @@ def decode(q, ks, vs, scale):
                 lse[b, h, s] = x.max() + math.log(np.exp(x - x.max()).sum()) if np.isfinite(x.max()) else np.nan
                 p = np.exp(x - lse[b, h, s])
                 o[b, s, h], w[b, s, h] = p @ vh[:m], p @ np.abs(vh[:m])
-                top[b, s, h] = (p @ np.abs(vh[:m]).reshape(m, -1, 32).max(-1)).repeat(32)
-    return o, lse, w, a, top
+    return o, lse, w, a
 
 
 def rope(x, pos, axes, freq, interleaved, sign=1):
