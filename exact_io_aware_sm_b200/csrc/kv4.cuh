@@ -58,11 +58,10 @@ __device__ __forceinline__ long long kv4_tile_at(const Kv4Pages& p, int b, int h
 // or a NaN.  m * (1/7) in fp32 rounds to the bf16 of the exact quotient: m
 // has 8 significant bits, so m / 7 is a bf16 value or at least 2^-12 of its
 // size away from every border between two.
-__device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t m) {
-  if (m >= 0x7f80u) return 0x7fffu;
-  if (m < 0x0d80u) return 0u;  // 2^-100
+__device__ __forceinline__ bool kv4_has_codes(uint32_t m) { return m - 0x0d80u < 0x7f80u - 0x0d80u; }  // finite, at least 2^-100
+__device__ __forceinline__ uint32_t kv4_scale_bits(uint32_t m, bool has_codes) {
   const float s = __uint_as_float(m << 16) * (1.f / 7.f);
-  return __bfloat16_as_ushort(__float2bfloat16_rn(s));
+  return has_codes ? __bfloat16_as_ushort(__float2bfloat16_rn(s)) : m < 0x7f80u ? 0u : 0x7fffu;
 }
 
 // Codes are 8 + floor(x / s + 1/2): x / s has a distance of 0 or at least 2^-9
@@ -79,8 +78,8 @@ __device__ __forceinline__ float kv4_inverse(uint32_t scale_bits) {
   return y;
 }
 
-// The codes of eight bf16 values (pairs, low half first), low nibbles first; scale and inverse of their group.
-__device__ __forceinline__ uint32_t kv4_codes(const uint32_t* w, uint32_t scale_bits, float inv) {
+// The codes of eight bf16 values (pairs, low half first), low nibbles first; inv is kv4_inverse of their group's scale.
+__device__ __forceinline__ uint32_t kv4_codes(const uint32_t* w, float inv) {
   auto sum = [&](int j, float m) {
     const uint32_t x = j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16;
     return __float_as_uint(fmaf(__uint_as_float(x), inv, m));
@@ -88,8 +87,7 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint32_t* w, uint32_t scale_
   // three codes at a time at bits 10, 14 and 18
   auto three = [&](int j) { return (sum(j, 12296.5f) & 0x3c00u) | (sum(j + 1, 776.5f) & 0x3c000u) | (sum(j + 2, 56.5f) & 0x3c0000u); };
   const uint32_t two = (sum(6, 12296.5f) & 0x3c00u) | (sum(7, 776.5f) & 0x3c000u);
-  const uint32_t c = three(0) >> 10 | three(3) << 2 | two << 14;
-  return scale_bits == 0u || scale_bits >= 0x7f80u ? 0x88888888u : c;
+  return three(0) >> 10 | three(3) << 2 | two << 14;
 }
 
 }  // namespace eio

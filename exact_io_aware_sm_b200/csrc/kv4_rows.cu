@@ -65,14 +65,13 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
 // The codes of eight channels (low nibbles first) of a group, and the group's scale, from four lanes' shares.
 __device__ __forceinline__ uint32_t narrow(const uint4& x, uint32_t* scale) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  uint32_t m = __vimax3_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
   m = max(m & 0xffffu, m >> 16);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  *scale = kv4_scale_bits(m);
-  return kv4_codes(w, *scale, kv4_inverse(*scale));  // infinities and NaNs have code 8 like the rest of their group
+  const bool codes = kv4_has_codes(m);
+  *scale = kv4_scale_bits(m, codes);
+  return codes ? kv4_codes(w, kv4_inverse(*scale)) : 0x88888888u;
 }
 
 // (c - 8) s of eight codes as bf16, rounded once.
