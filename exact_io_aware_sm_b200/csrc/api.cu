@@ -20,6 +20,7 @@
 
 #include "../../include/attn.h"
 #include "kernels.h"
+#include "kernels_kv4.h"
 #include "plan.h"
 
 namespace {

@@ -9,7 +9,7 @@
 #include <vector>
 
 #include "../../include/attn.h"
-#include "kernels.h"
+#include "kernels_kv4.h"
 #include "kv4.cuh"
 
 namespace {

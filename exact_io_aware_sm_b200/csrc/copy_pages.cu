@@ -6,7 +6,7 @@
 // No destination is also a source or named twice (the caller of the launcher
 // has checked), so the copies are independent.  Memory bound: every byte is
 // read once and written once.
-#include "kernels.h"
+#include "kernels_kv4.h"
 
 namespace eio {
 namespace {

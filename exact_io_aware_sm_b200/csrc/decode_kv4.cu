@@ -49,7 +49,7 @@
 
 #include <type_traits>
 
-#include "kernels.h"
+#include "kernels_kv4.h"
 #include "kv4.cuh"
 #include "pdl.cuh"
 #include "ptx_sm100.cuh"

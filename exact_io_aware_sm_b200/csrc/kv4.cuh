@@ -26,7 +26,7 @@
 
 #include <cstdint>
 
-#include "kernels.h"
+#include "kernels_kv4.h"
 
 namespace eio {
 

@@ -17,7 +17,7 @@
 // to widen.
 #include <cuda_bf16.h>
 
-#include "kernels.h"
+#include "kernels_kv4.h"
 #include "kv4.cuh"
 
 namespace eio {

@@ -19,7 +19,7 @@
 // eight pairs) with 16-byte loads and stores, four such pieces of work in flight.
 #include <cuda_bf16.h>
 
-#include "kernels.h"
+#include "kernels_kv4.h"
 
 namespace eio {
 namespace {
