@@ -427,8 +427,10 @@ int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, cons
  *   lse  device, fp32 [B, Hq, Sq] (written); may be NULL
  *   workspace  device, attn_decode_kv4_workspace() bytes; its content need not be
  *              kept or cleared.  Calls that may run at the same time need one each.
- * Any Hq % Hkv == 0 and any Sq.  A row that sees no token gets O = 0, LSE = -inf.  A query row
- * that holds an infinity or a NaN gives NaN.  The result does not depend on timing.
+ * Any Hq % Hkv == 0 and any Sq (a KV head's (head, token) pairs go in blocks of 8, and each
+ * block reads the cache).  A row that sees no token gets O = 0, LSE = -inf.  A query row that
+ * holds an infinity, a NaN or a magnitude of 2^114 or more gives NaN.  The result does not
+ * depend on timing.
  * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE; a bounded wait that
  * runs out latches ATTN_ERR_DEVICE_TIMEOUT.
  */

@@ -335,7 +335,10 @@ DECODE_CASES = [
     ([0, 0], 1, 2, 1, 64, 32), ([65, 300, 2], 4, 4, 2, 128, 32), ([513, 64, 127, 1], 2, 3, 3, 64, 64),
     ([900, 3], 8, 8, 1, 128, 128), ([777], 5, 7, 2, 64, 256), ([1500, 20], 3, 5, 1, 128, 64),
     ([700, 0, 48], 1, 8, 2, 128, 256), ([260] * 40, 1, 2, 3, 64, 16), ([90, 41], 17, 1, 2, 64, 16),
-    ([3000], 1, 16, 1, 128, 64), ([130, 70], 1, 12, 1, 64, 32), ([2049], 2, 6, 1, 128, 16)]
+    ([3000], 1, 16, 1, 128, 64), ([130, 70], 1, 12, 1, 64, 32), ([2049], 2, 6, 1, 128, 16),
+    # one unit over every CTA; many short sequences, empty ones among them; more columns than one block
+    ([20000], 1, 3, 1, 64, 64), ([(7 * i) % 50 * (i % 3 > 0) for i in range(150)], 1, 2, 2, 64, 16),
+    ([33, 1, 64], 9, 2, 1, 64, 32), ([100, 31], 8, 8, 1, 128, 64)]
 
 
 @pytest.mark.parametrize("case", DECODE_CASES)
@@ -513,6 +516,86 @@ def test_decode_equals_attention_over_the_rows_read_back():
     e = 2.0 ** -8 * a.transpose(0, 2, 1)[..., None]
     assert (np.abs(f64(o) - f64(of)) <= (4 * 2.0 ** -8 + 2 * (np.exp(2 * e) - 1)) * w).all()
     assert (np.abs(f64(lse) - f64(lf)) <= 2.0 ** -8 * a + 1e-3).all()
+
+
+def test_a_step_in_a_graph_follows_its_buffers():
+    """Rotation, append, page copy, read and decode captured once and replayed with other rows, positions
+    and lengths in the same buffers."""
+    B, H, G, d, page = 2, 2, 4, 64, 16
+    axes, freq = _rope_table((16, 16), 2)
+    table, pages, n_pages = _table([64, 64], page, 3, extra=4)
+    free = sorted(set(range(n_pages)) - set(sum(pages, [])))
+    pool = _pool(n_pages, H, d, page, 4)
+    t, lens = i32(table), i32([40, 10])
+    q, k, v = (randn((B, 1, h, d), 5 + h) for h in (G * H, H, H))
+    pos = i32(np.zeros((B, 1, 2)))
+
+    def step():
+        rq, rk = eio.rope(q, k, pos, axes, freq)
+        eio.kv4_append(rk, v, pool, t, lens)
+        eio.copy_pages(pool, [pages[0][0]], [free[0]])
+        return (rq, rk, *eio.attn_decode_kv4(rq, pool, t, lens), *eio.kv4_read(pool, t, lens, 7, d))
+    eio.kv4_append(randn((B, 64, H, d), 1), randn((B, 64, H, d), 2), pool, t, i32([64, 64]))
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for i, n in enumerate(([41, 11], [64, 1], [17, 16])):
+        for x, seed in ((q, 30), (k, 40), (v, 50)):
+            x.copy_(randn(x.shape, seed + i))
+        lens.copy_(i32(n))
+        pos.fill_(7 + 1000 * i)
+        before = pool.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        got, after = [x.clone() for x in out], pool.clone()
+        pool.copy_(before)
+        for x, y in zip(got, step()):
+            assert torch.equal(x, y)
+        assert torch.equal(after, pool) and torch.equal(pool[free[0]], pool[pages[0][0]])
+    eio.sync_status()
+
+
+def test_first_call_on_a_device_inside_a_capture_is_refused():
+    """The error word is allocated by the first call: inside a capture that is an error, not a broken capture."""
+    pool, table, n, _, _ = _cache_of([20], 1, 64, 16, 91)
+    q = randn((1, 1, 1, 64), 1)
+    want = eio.attn_decode_kv4(q, pool, table, n)
+    torch.cuda.synchronize()
+    eio.shutdown()
+    x = torch.zeros(4, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(eio.AttnError) as e:
+            eio.kv4_append(q, q, pool, table, n)
+        x += 1
+    assert e.value.code == 8
+    g.replay()
+    assert (x == 1).all()
+    got = eio.attn_decode_kv4(q, pool, table, n)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_pools_past_four_gigabytes():
+    """Pages whose bytes lie past 2^32 are written, read, decoded and copied like the first ones."""
+    H, d, page, n_pages = 8, 128, 256, 16000
+    pool = eio.kv4_pool(n_pages, H, d, page)
+    assert (n_pages - 8) * pool[0].numel() > 2 ** 32
+    far, near = [n_pages - 1, n_pages - 3], [1, 0]
+    lens = [300]
+    k, v = randn((1, 300, H, d), 1), randn((1, 300, H, d), 2)
+    q = randn((1, 2, 2 * H, d), 3)
+    got = []
+    for pages in (far, near):
+        t, n = i32([pages]), i32(lens)
+        eio.kv4_append(k, v, pool, t, n)
+        got.append((*eio.kv4_read(pool, t, n, 300, d), *eio.attn_decode_kv4(q, pool, t, n)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    eio.copy_pages(pool, far, [n_pages - 7, 2])
+    assert torch.equal(pool[2], pool[far[1]]) and torch.equal(pool[n_pages - 7], pool[far[0]])
+    assert torch.equal(eio.attn_decode_kv4(q, pool, i32([[n_pages - 7, 2]]), i32(lens))[0], got[0][2])
+    eio.sync_status()
 
 
 # ------------------------------------------------------------------ pages
