@@ -61,6 +61,7 @@ namespace {
 constexpr int kMaxCtas = 148;
 constexpr int kUnitCost = 3;  // of a unit's start and end, in stages (measured: 1 to 4)
 constexpr int kRingBudget = 222 * 1024;
+constexpr int kMostIdle = 1 << 24;  // rounds (of 100 ns or so) in which no stage was taken
 constexpr int kCombineThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kMostWeight = 256.f;  // of a lane's four keys of a column, relative to the base: more moves the base
@@ -292,8 +293,15 @@ __device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Colum
     const int id = pg.table[static_cast<size_t>(b) * pg.max_pages + p];
     return static_cast<unsigned>(id) < static_cast<unsigned>(pg.n_pages) ? id : -1;
   };
-  // Ids are read ahead: of the page (for pages of one tile, of both tiles) of the next stage, and of the page after.
-  int id = 0, id_next = 0, id_first = 0;
+  // Where the next stage is: id its page, src its tiles there, in_page the stages that the page still has; pages of
+  // one tile have half a stage each, id and id_next.  Ids are read a page (a stage) ahead.
+  int id = 0, id_next = 0, id_first = 0, in_page = 0;
+  const uint8_t* src = nullptr;
+  const long long head_bytes = static_cast<long long>(C::kTile) << tiles_shift;
+  auto enter_page = [&](int tile) {
+    src = pg.pool + max(id, 0) * page_bytes + h * head_bytes + tile * C::kTile;
+    in_page = ((1 << tiles_shift) - tile) >> 1;
+  };
   auto look = [&]() {
     const int p = (st * C::kKeys) >> pg.page_shift;
     id = page_id(p);
@@ -302,40 +310,40 @@ __device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Colum
   if (left > 0) {
     look();
     id_first = st == 0 ? id : page_id(0);
+    enter_page((st * 2) & ((1 << tiles_shift) - 1));
   }
-  bool fresh = true;  // the next stage is its run's first of a unit
-  int issued = 0, slot = 0;
+  const bool small_pages = tiles_shift == 0;
+  int unit = h * cols.blocks + cb;
+  int fresh = 1;  // the next stage is its run's first of a unit
+  int issued = 0, slot = 0, idle = 0;
   uint32_t phase = 1;  // parity of the slot's last release; the first round finds every slot free
-  uint64_t since = globaltimer_ns();
   while (__any_sync(0xffffffffu, left > 0)) {
     const bool go = left > 0 && mbar_test(&free_[slot], phase);
     if (go) {
-      const int k0 = st * C::kKeys, ntiles = len - k0 > 16 ? 2 : 1;
+      const int k0 = st * C::kKeys, this_unit = unit, this_b = b, this_len = len;
+      const bool two = len - k0 > 16;
       uint8_t* dst = ring + slot * C::kStage;
-      const uint8_t *src0 = nullptr, *src1 = nullptr;
-      uint32_t bytes0 = ntiles * C::kTile;
-      int bad;
-      if (tiles_shift > 0) {
-        bad = id < 0 ? 3 : 0;
-        if (id >= 0) src0 = pg.pool + id * page_bytes + ((static_cast<long long>(h) << tiles_shift) + ((k0 >> 4) & ((1 << tiles_shift) - 1))) * C::kTile;
-      } else {  // pages of one tile
-        bad = (id < 0 ? 1 : 0) | (id_next < 0 && ntiles == 2 ? 2 : 0);
-        bytes0 = C::kTile;
-        if (id >= 0) src0 = pg.pool + id * page_bytes + static_cast<long long>(h) * C::kTile;
-        if (id_next >= 0 && ntiles == 2) src1 = pg.pool + id_next * page_bytes + static_cast<long long>(h) * C::kTile;
-      }
-      if (bad) atomicCAS(pg.err, 0, kErrDeviceArg);
-      const int this_b = b, this_u = h * cols.blocks + cb, this_len = len;
-      int flags = (fresh ? 1 : 0) | bad << 2;
-      fresh = false;
+      uint64_t* bar = &full[slot];
+      int bad = id < 0 ? 3 : 0;
+      if (small_pages) bad = (id < 0 ? 1 : 0) | (two && id_next < 0 ? 2 : 0);
       --left;
       ++st;
       if (st == nst) left = max(left - kUnitCost, 0);  // the next unit's start
-      if (st == nst || left == 0) flags |= 2;
-      meta[slot] = make_int4(this_b, this_u, k0 | flags, left == 0 ? this_len | static_cast<int>(0x80000000u) : this_len);
-      mbar_arrive_expect_tx(&full[slot], (src0 ? bytes0 : 0u) + (src1 ? C::kTile : 0u));
-      if (src0) bulk_load(dst, src0, bytes0, &full[slot]);
-      if (src1) bulk_load(dst + C::kTile, src1, C::kTile, &full[slot]);
+      const int flags = fresh | (st == nst || left == 0 ? 2 : 0) | bad << 2;
+      fresh = 0;
+      meta[slot] = make_int4(this_b, this_unit, k0 | flags, left == 0 ? this_len | static_cast<int>(0x80000000u) : this_len);
+      if (!small_pages) {
+        const uint32_t bytes = bad ? 0u : two ? C::kStage : C::kTile;
+        mbar_arrive_expect_tx(bar, bytes);
+        if (bytes) bulk_load(dst, src, bytes, bar);
+      } else {
+        const bool one = id >= 0, other = two && id_next >= 0;
+        mbar_arrive_expect_tx(bar, (one + other) * C::kTile);
+        if (one) bulk_load(dst, src, C::kTile, bar);
+        if (other) bulk_load(dst + C::kTile, pg.pool + id_next * page_bytes + h * head_bytes, C::kTile, bar);
+      }
+      if (bad) atomicCAS(pg.err, 0, kErrDeviceArg);
+      src += C::kStage;
       ++issued;
       if (++slot == R) {
         slot = 0;
@@ -344,40 +352,42 @@ __device__ __forceinline__ void bring_stages(const DecodeKv4Args& a, const Colum
       if (left > 0) {
         if (st == nst) {  // the next unit, in the next sequence that has one
           st = 0;
-          fresh = true;
-          bool moved = false;
+          fresh = 1;
+          ++unit;
           if (++cb == cols.blocks) {
             cb = 0;
             if (++h == pg.Hkv) {
-              h = 0;
-              moved = true;
+              h = unit = 0;
               do {
                 ++b;
                 len = b < pg.B ? checked_len(pg, b) : 1;  // past the end only where lengths changed under the call
               } while (len == 0);
               b = min(b, pg.B - 1);
               nst = (len + C::kKeys - 1) / C::kKeys;
+              id_first = page_id(0);
             }
           }
-          if (moved) id_first = page_id(0);
           id = id_first;
           id_next = page_id(1);
-        } else if (tiles_shift == 0) {
+          enter_page(0);
+        } else if (small_pages) {
           look();
-        } else if (((st * C::kKeys) & ((1 << pg.page_shift) - 1)) == 0) {
+          enter_page(0);
+        } else if (--in_page == 0) {
           id = id_next;
           id_next = page_id(((st * C::kKeys) >> pg.page_shift) + 1);
+          enter_page(0);
         }
       }
     }
     if (__any_sync(0xffffffffu, go)) {
-      since = globaltimer_ns();
+      idle = 0;
     } else {
-      if (globaltimer_ns() - since > kWaitLimitNs) {
+      if (++idle > kMostIdle) {
         if (lane == 0) atomicCAS(pg.err, 0, kErrDeviceTimeout);
         break;
       }
-      __nanosleep(100);
+      __nanosleep(20);
     }
   }
   // Every copy lands before the CTA retires.
