@@ -15,8 +15,11 @@
 //
 // Memory bound: q and k are read and written once.  A block takes a run of
 // tokens; it computes the cosines and sines of its (token, pair)s once into
-// shared memory (for every head), then its threads stream over (token, head,
-// eight pairs) with 16-byte loads and stores, four such pieces of work in flight.
+// shared memory (for every head) while the first pieces of work (token, head, eight
+// pairs) are on their way, then its threads stream over them with 16-byte loads and
+// stores, four pieces in flight.  24960 tokens of 48 heads of 128 (613 MB): 98 us alone,
+// 6.2 TB/s of the 6.46 that a copy reaches (112 when the interleaved form read
+// 32 bytes a thread in two halves); the GPT-2 training step's q and k (25 MB), cold: 13.
 #include <cuda_bf16.h>
 
 #include "kernels_kv4.h"
