@@ -382,6 +382,12 @@ def _apart(out, name, others):
         raise ValueError(f"{name} overlaps another tensor of the call")
 
 
+def _like(t):
+    """A contiguous tensor of t's shape and type."""
+    import torch
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 _PACK10, _PACK4 = struct.Struct("10q").pack, struct.Struct("4q").pack  # strides, as the library reads them
 
 
@@ -424,14 +430,14 @@ def rope(q, k, positions, axes, freq, interleaved=False, inverse=False, q_out=No
     if A > 1 and pa != 1:
         raise ValueError("positions must be contiguous in its last dimension")
     if q_out is None:
-        q_out = torch.empty((B, N, Hq, d), dtype=dtype, device=q.device)
+        q_out = _like(q)
         qob, qon = N * Hq * d, Hq * d
     else:
         qob, qon = _rows(q_out, "q_out", (B, N, Hq, d), dtype, dev)
         _apart(q_out, "q_out", [(q, True), (positions, False)] + ([] if k is None else [(k, False)]))
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((B, N, Hk, d), dtype=dtype, device=q.device)
+            k_out = _like(k)
             kob, kon = N * Hk * d, Hk * d
         else:
             kob, kon = _rows(k_out, "k_out", (B, N, Hk, d), dtype, dev)
@@ -526,11 +532,11 @@ def kv4_read(pool, table, seqlens, N, d, start=None, k=None, v=None, stream=None
     B = table.shape[0]
     shape, bf16 = (B, N, Hkv, d), torch.bfloat16
     if k is None:
-        k = torch.empty(shape, dtype=bf16, device=pool.device)
+        k = pool.new_empty(shape, dtype=bf16)
     elif not _is(k, shape, bf16, dev):
         _need(k, "k", shape, (bf16,), pool.device)
     if v is None:
-        v = torch.empty(shape, dtype=bf16, device=pool.device)
+        v = torch.empty_like(k)
     elif not _is(v, shape, bf16, dev):
         _need(v, "v", shape, (bf16,), pool.device)
     rc = lib().attn_kv4_read(k.data_ptr(), v.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(),
@@ -565,11 +571,11 @@ def attn_decode_kv4(q, pool, table, seqlens, o=None, lse=None, scale=None, strea
         _need(o, "o", shape, (bf16,), q.device)
     if lse is None:
         if want_lse:
-            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, Hq, Sq), dtype=torch.float32)
     elif not _is(lse, (B, Hq, Sq), torch.float32, dev):
         _need(lse, "lse", (B, Hq, Sq), (torch.float32,), q.device)
     n = _decode_kv4_workspace(B, Sq, Hq, Hkv, d, page, max_pages)
-    work = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    work = pool.new_empty(n) if n else None
     rc = lib().attn_decode_kv4(q.data_ptr(), pool.data_ptr(), table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
                                None if lse is None else lse.data_ptr(), None if work is None else work.data_ptr(), n,
                                B, Sq, Hq, Hkv, d, n_pages, page, max_pages,

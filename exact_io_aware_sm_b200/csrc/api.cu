@@ -347,13 +347,16 @@ int eio::device_error_word(cudaStream_t s, int** out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_err(e, "cudaGetDevice");
   const auto it = g_ws.find(dev);
-  if (it == g_ws.end() || !it->second.d_err) {
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    e = cudaStreamIsCapturing(s, &st);
-    if (e != cudaSuccess) return cuda_err(e, "cudaStreamIsCapturing");
-    if (st != cudaStreamCaptureStatusNone)
-      return set_err(ATTN_ERR_WORKSPACE, "the first call on a device allocates its error word: make it before a capture");
+  if (it != g_ws.end() && it->second.d_err) {  // allocated by a call that found the device to be one of ours
+    *out = it->second.d_err;
+    return ATTN_OK;
   }
+  if (int rc = check_device_sm100()) return rc;
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  e = cudaStreamIsCapturing(s, &st);
+  if (e != cudaSuccess) return cuda_err(e, "cudaStreamIsCapturing");
+  if (st != cudaStreamCaptureStatusNone)
+    return set_err(ATTN_ERR_WORKSPACE, "the first call on a device allocates its error word: make it before a capture");
   DevWs* ws;
   if (int rc = get_ws(&ws)) return rc;
   *out = ws->d_err;

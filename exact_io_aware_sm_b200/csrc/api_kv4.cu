@@ -59,10 +59,7 @@ int check_rows(int B, int N, int Hkv) {
   return ATTN_OK;
 }
 
-int ready(void* stream, int** err) {
-  if (int rc = require_sm100()) return rc;
-  return device_error_word(static_cast<cudaStream_t>(stream), err);
-}
+int ready(void* stream, int** err) { return device_error_word(static_cast<cudaStream_t>(stream), err); }
 
 }  // namespace
 
@@ -96,10 +93,12 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
     if (!(std::fabs(freq[p]) <= kRopeMaxFreq))
       return fail(ATTN_ERR_SHAPE, "freq[%d] must be finite and at most %g in magnitude", p, kRopeMaxFreq);
     // turns per position, modulo 1, as a 64-bit fraction
-    const long double turns = static_cast<long double>(freq[p]) / 6.283185307179586476925286766559005768L;
-    const long double f = turns - std::floor(turns);
-    const long double bits = f * 18446744073709551616.0L;
-    a.freq[p] = bits >= 18446744073709551616.0L ? 0ull : static_cast<unsigned long long>(bits);
+    long double turns = static_cast<long double>(freq[p]) * 0.159154943091895335768883763372514362L;  // 1 / 2 pi
+    turns -= static_cast<long double>(static_cast<long long>(turns));
+    if (turns < 0) turns += 1;
+    const long double high = turns * 4294967296.0L;
+    const unsigned long long hi = static_cast<unsigned long long>(static_cast<long long>(high));
+    a.freq[p] = (hi << 32) + static_cast<unsigned long long>(static_cast<long long>((high - static_cast<long double>(hi)) * 4294967296.0L));
     a.axis[p] = axes[p];
   }
   if (int rc = require_sm100()) return rc;

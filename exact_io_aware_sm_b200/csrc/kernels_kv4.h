@@ -67,8 +67,8 @@ size_t decode_kv4_workspace_bytes(int B, int Sq, int Hq, int Hkv, long long max_
 cudaError_t launch_copy_pages(void* pool, long long page_bytes, const int* src, const int* dst, int n, cudaStream_t s);
 
 // The current device's error word (the one attn_sync_status reads), for calls
-// on stream s; an attn_status.  Allocated at a device's first call, which is
-// refused while s is captured.
+// on stream s; an attn_status (ATTN_ERR_UNSUPPORTED on a device that is not sm_100).
+// Allocated at a device's first call, which is refused while s is captured.
 int device_error_word(cudaStream_t s, int** out);
 
 }  // namespace eio

@@ -370,8 +370,8 @@ int attn_fwd_bound(const void* q, const void* k, const void* v, void* o, float* 
  * freq[p]: (x, y) -> (x cos - y sin, x sin + y cos).  The pair is channels p and
  * p + d / 2, or 2p and 2p + 1 (interleaved != 0); other channels are copied.
  * inverse != 0 rotates by -theta, which is also the gradient's map.  theta is
- * reduced in 64-bit fixed point: its error is below |position| * 2^-63 turns,
- * whatever the position.
+ * reduced in 64-bit fixed point: its error is below 2^-62 of itself and |position| *
+ * 2^-64 turns together, whatever the position.
  *   q, q_out   device, [B, N, Hq, d] (dtype); k, k_out  device, [B, N, Hk, d], Hk may be 0
  *              q_out may be q (k_out may be k) with the same strides
  *   positions  device, int32 [B, N, n_axes], the last dimension contiguous
