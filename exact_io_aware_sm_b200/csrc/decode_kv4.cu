@@ -895,12 +895,12 @@ __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(con
   const int tid = threadIdx.x;
   pdl_wait();  // the first kernel has finished and its slots are visible
   const Run run = runs[i];
-  const long long total = runs[ctas].x, before = runs[i - 1].x;
+  const long long total = runs[ctas].x, before = runs[i - 1].x, later = runs[min(tid + i, ctas)].x;
   // The first stage of the unit at the boundary; the boundary is the unit's first one, or another CTA's.
   const long long first = run.x - run.st;
   if (run.x >= total || run.st == 0 || first < before) return;
   // It has parts in CTA i - 1 and in every later one that starts inside it.
-  const int n = 1 + __syncthreads_count(tid + i < ctas && runs[min(tid + i, ctas)].x < first + run.nst);
+  const int n = 1 + __syncthreads_count(tid + i < ctas && later < first + run.nst);
   const int late = before + kUnitCost < first ? 1 : 0;  // the unit starts after CTA i - 1's run does
   const int heads = a.Hq / a.pages.Hkv, live_cols = heads * a.Sq;
   const int uh = run.u / cols.blocks, c0 = (run.u - uh * cols.blocks) * cols.per;
