@@ -51,11 +51,11 @@ int check_pages(int B, int Hkv, int d, int n_pages, int page, int max_pages, Kv4
   return ATTN_OK;
 }
 
-// Rows that an append or a read covers: a warp each 16 of a head, in a grid of at most 2^31 - 1 blocks.
+// Rows that an append or a read covers: a warp each 16 of a head, four to a block, at most 2^31 - 1 blocks.
 int check_rows(int B, int N, int Hkv) {
   if (N < 1 || static_cast<long long>(B) * N >= (1ll << 31))
     return fail(ATTN_ERR_SHAPE, "N must be >= 1 and B * N below 2^31");
-  if (static_cast<double>(B) * (N / 16 + 2) * Hkv >= 8589934592.0) return fail(ATTN_ERR_SHAPE, "too many rows");
+  if (B * ((N / 16 + 2.0) * Hkv / 4 + 1) >= 2147483648.0) return fail(ATTN_ERR_SHAPE, "too many rows");
   return ATTN_OK;
 }
 

@@ -15,7 +15,7 @@
 // Both are memory bound: per token and head 4 d bytes of bf16 rows and d + d / 8
 // bytes of cache.  Narrowing is bound by the integer pipe as well (about 9 instructions a
 // value with the group's maximum and scale).  16384 tokens of 8 heads of 128 (86 MB each
-// way, 13.3 us at the rate of a copy): append 20.6 us, read 15.0; a thread a group of 32
+// way, 13.3 us at the rate of a copy): append 19.1 us, read 15.4; a thread a group of 32
 // channels, with its scattered stores, took 58 for both.
 #include <cuda_bf16.h>
 
@@ -35,16 +35,15 @@ struct TileAt {
   bool ok;
 };
 
-__device__ __forceinline__ TileAt my_tile(int B, int Hkv, int N) {
-  const long long w = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int per = tiles_of(N);
-  const long long bt = w / Hkv;
-  TileAt x;
-  x.h = static_cast<int>(w - bt * Hkv);
-  x.b = static_cast<int>(bt / per);
-  x.tile = static_cast<int>(bt - static_cast<long long>(x.b) * per);
-  x.ok = x.b < B;
-  return x;
+// Blocks of a sequence: a warp each (tile, head).
+__host__ __device__ constexpr unsigned blocks_of(int N, int Hkv) {
+  return (static_cast<unsigned>(tiles_of(N)) * static_cast<unsigned>(Hkv) + kRowWarps - 1) / kRowWarps;
+}
+
+__device__ __forceinline__ TileAt my_tile(int Hkv, int N) {
+  const unsigned blocks = blocks_of(N, Hkv), b = blockIdx.x / blocks;
+  const unsigned i = (blockIdx.x - b * blocks) * kRowWarps + (threadIdx.x >> 5), tile = i / static_cast<unsigned>(Hkv);
+  return {static_cast<int>(b), static_cast<int>(tile), static_cast<int>(i - tile * Hkv), tile < static_cast<unsigned>(tiles_of(N))};
 }
 
 // A lane's group words [G] to or from 4 G consecutive bytes.
@@ -64,16 +63,33 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-// The codes of eight channels (low nibbles first) of a group, and the group's scale, from four lanes' shares.
-__device__ __forceinline__ uint32_t narrow(const uint4& x, uint32_t* scale) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = __vimax3_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-  m = max(m & 0xffffu, m >> 16);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const bool codes = kv4_has_codes(m);
-  *scale = kv4_scale_bits(m, codes);
-  return codes ? kv4_codes(w, kv4_inverse(*scale)) : 0x88888888u;
+// The largest magnitudes of a lane's eight channels of a group, two at a time in the halves of a word.
+__device__ __forceinline__ uint32_t largest8(const uint4& x) {
+  return __vimax3_u16x2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+}
+
+// A row of G groups, eight channels of each here and the others in three more lanes: the codes of the eight (low
+// nibbles first) and the scales, two groups to a word.
+template <int G>
+__device__ __forceinline__ void narrow(const uint4* x, uint32_t* codes, uint32_t* scales) {
+#pragma unroll
+  for (int i = 0; i < G / 2; ++i) {
+    const uint32_t a = largest8(x[2 * i]), b = largest8(x[2 * i + 1]);
+    uint32_t m = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));  // of the first group, of the second
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    uint32_t s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t mk = k ? m >> 16 : m & 0xffffu;
+      const bool has = kv4_has_codes(mk);
+      s[k] = kv4_scale_bits(mk, has);
+      const uint4& u = x[2 * i + k];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      codes[2 * i + k] = has ? kv4_codes(w, kv4_inverse(s[k])) : 0x88888888u;
+    }
+    scales[i] = __byte_perm(s[0], s[1], 0x5410);
+  }
 }
 
 // (c - 8) s of eight codes as bf16, rounded once.
@@ -93,7 +109,7 @@ __device__ __forceinline__ uint4 widen(uint32_t w, uint32_t scale) {
 template <int D>
 __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4AppendArgs a) {
   constexpr int G = D / 32;
-  const TileAt x = my_tile(a.pages.B, a.pages.Hkv, a.N);
+  const TileAt x = my_tile(a.pages.Hkv, a.N);
   if (!x.ok) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // The tokens that sequence b appends: rows 0 .. n - 1 of k and v, positions len - n .. len - 1.
@@ -125,21 +141,19 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4App
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int tok = g + 8 * r;
-    uint32_t w[G], s[G];
-#pragma unroll
-    for (int grp = 0; grp < G; ++grp) w[grp] = narrow(in[0][r][grp], &s[grp]);
+    uint32_t w[G], s[G / 2];
+    narrow<G>(in[0][r], w, s);
     if (live[r]) {
       store_words<G>(tile + (tok * 4 + t) * (4 * G), w);
       if (t == 0) {
 #pragma unroll
-        for (int i = 0; i < G / 2; ++i) *reinterpret_cast<uint32_t*>(tile + kv4_off_ks(D) + tok * (2 * G) + 4 * i) = s[2 * i] | s[2 * i + 1] << 16;
+        for (int i = 0; i < G / 2; ++i) *reinterpret_cast<uint32_t*>(tile + kv4_off_ks(D) + tok * (2 * G) + 4 * i) = s[i];
       }
     }
-#pragma unroll
-    for (int grp = 0; grp < G; ++grp) w[grp] = narrow(in[1][r][grp], &s[grp]);
+    narrow<G>(in[1][r], w, s);
     if (live[r] && t == 1) {
 #pragma unroll
-      for (int i = 0; i < G / 2; ++i) *reinterpret_cast<uint32_t*>(tile + kv4_off_vs(D) + tok * (2 * G) + 4 * i) = s[2 * i] | s[2 * i + 1] << 16;
+      for (int i = 0; i < G / 2; ++i) *reinterpret_cast<uint32_t*>(tile + kv4_off_vs(D) + tok * (2 * G) + 4 * i) = s[i];
     }
     // The lane of an even token takes channels 8 t .. 8 t + 3 of both tokens of the pair, that of the odd one the rest.
     const int odd = g & 1;
@@ -163,7 +177,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4App
 template <int D>
 __global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4ReadArgs a) {
   constexpr int G = D / 32;
-  const TileAt x = my_tile(a.pages.B, a.pages.Hkv, a.N);
+  const TileAt x = my_tile(a.pages.Hkv, a.N);
   if (!x.ok) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   int len = a.pages.seqlens[x.b], start = a.start ? a.start[x.b] : 0;
@@ -217,10 +231,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4ReadA
 }
 
 template <typename A>
-unsigned row_blocks(const A& a) {
-  const long long warps = static_cast<long long>(a.pages.B) * tiles_of(a.N) * a.pages.Hkv;
-  return static_cast<unsigned>((warps + kRowWarps - 1) / kRowWarps);
-}
+unsigned row_blocks(const A& a) { return static_cast<unsigned>(a.pages.B) * blocks_of(a.N, a.pages.Hkv); }
 
 }  // namespace
 
