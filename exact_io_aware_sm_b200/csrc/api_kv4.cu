@@ -51,11 +51,12 @@ int check_pages(int B, int Hkv, int d, int n_pages, int page, int max_pages, Kv4
   return ATTN_OK;
 }
 
-// Rows that an append or a read covers: a warp each 16 of a head, four to a block, at most 2^31 - 1 blocks.
+// Rows that an append or a read covers: a warp each 16 of a head, numbered in 32 bits; positions of rows stay in them too.
 int check_rows(int B, int N, int Hkv) {
-  if (N < 1 || static_cast<long long>(B) * N >= (1ll << 31))
-    return fail(ATTN_ERR_SHAPE, "N must be >= 1 and B * N below 2^31");
-  if (B * ((N / 16 + 2.0) * Hkv / 4 + 1) >= 2147483648.0) return fail(ATTN_ERR_SHAPE, "too many rows");
+  if (N < 1 || N > kKv4MaxTokens || static_cast<long long>(B) * N >= (1ll << 31))
+    return fail(ATTN_ERR_SHAPE, "N must be 1 to 2^30 and B * N below 2^31");
+  if (B * ((N / 16 + 2.0) * Hkv + 4) >= 2147483648.0)
+    return fail(ATTN_ERR_SHAPE, "too many rows: B * (N / 16 + 2) * Hkv must be below 2^31");
   return ATTN_OK;
 }
 

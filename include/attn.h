@@ -399,6 +399,7 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
  * not read, and no other byte of the pool changes.  A count outside [0, min(N,
  * seqlens[b])] latches ATTN_ERR_DEVICE_ARG and appends nothing to that sequence.  No
  * two appended tokens may share a page slot (a page in two tables is copied first).
+ * Limits: N at most 2^30, B * N and B * (N / 16 + 2) * Hkv below 2^31.
  * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE.
  */
 int attn_kv4_append(const void* k, const void* v, void* pool, const int32_t* table, const int32_t* seqlens,
@@ -412,7 +413,7 @@ int attn_kv4_append(const void* k, const void* v, void* pool, const int32_t* tab
  *          start[b] + i, bf16((c - 8) s); zeros at and past seqlens[b]
  *   start  device int32 [B], or NULL (0); a negative one latches ATTN_ERR_DEVICE_ARG
  *          and its sequence reads as zeros
- * Errors: as attn_kv4_append.
+ * Limits and errors: as attn_kv4_append.
  */
 int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, const int32_t* seqlens,
                   const int32_t* start, int B, int N, int Hkv, int d, int n_pages, int page, int max_pages,

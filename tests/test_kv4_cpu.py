@@ -83,6 +83,14 @@ def test_read_refusals(code, kw):
     assert _read(**kw) == code and eio.last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(N=(1 << 30) + 1), dict(N=(1 << 31) - 1), dict(N=1 << 21, H=65535),
+                                dict(B=8, N=1 << 20, H=5000)])
+@pytest.mark.parametrize("call", [_append, _read])
+def test_rows_past_32_bits_are_refused(call, kw):
+    """Row positions and warps are numbered in 32 bits; broadcast rows reach such sizes without the memory."""
+    assert call(**kw) == 2 and eio.last_error()
+
+
 def _decode(**kw):
     a = dict(q=FAKE, pool=FAKE, table=FAKE, lens=FAKE, o=FAKE, lse=None, work=FAKE, n=1 << 40, B=1, Sq=1, Hq=4, H=2,
              d=64, n_pages=8, page=16, mp=4, scale=0.1)
