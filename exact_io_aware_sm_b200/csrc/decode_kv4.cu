@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const int e = min(max(141 - static_cast<int>(mx >> 7), -100), 100);  // q 2^e
-    const float fc = a.scale_log2 * pow2(24 - e);
+    // Positive and finite, so that masked scores (-inf) and scores of 0 stay what they are whatever the scale.
+    const float fc = fminf(fmaxf(a.scale_log2 * pow2(24 - e), pow2(-126)), 3.0e38f);
     // Codes n and n + 4 of a word sit 16 bits apart; odd n are masked 4 bits higher, 16 times as large.
     const uint32_t up = static_cast<uint32_t>(127 + e) << 7 | static_cast<uint32_t>(123 + e) << 23;  // bf16 2^e, 2^(e - 4)
     float x0 = 0.f, x1 = 0.f;

@@ -365,6 +365,18 @@ def test_decode_of_small_and_large_queries(size, d):
     _decode_close(o, lse, q, ks, vs, 0.25)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_with_a_scale_near_zero(d):
+    """Weights are equal whatever the queries, zero rows among them, and masked tokens still have none."""
+    lens = [0, 1, 3, 70]
+    pool, table, n, ks, vs = _cache_of(lens, 2, d, 16, 23)
+    q = randn((4, 3, 4, d), 6)
+    q[:, :, 1] = 0
+    for scale in (1e-10, 1e-25, 1e-37):
+        o, lse = eio.attn_decode_kv4(q, pool, table, n, scale=scale)
+        _decode_close(o, lse, q, ks, vs, scale)
+
+
 def test_decode_masked_tokens_with_nan_do_not_matter():
     """A NaN in a token that only the newest query sees leaves the others as they were; that one is NaN."""
     d, page, H, L = 128, 32, 2, 70
