@@ -388,6 +388,16 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
+def _axes(axes):
+    """Axis numbers as a uint8 array, refused where that would change them."""
+    axes = np.asarray(axes)
+    if axes.dtype == np.uint8:
+        return axes
+    if axes.size and (not np.issubdtype(axes.dtype, np.integer) or axes.min() < 0 or axes.max() > 255):
+        raise ValueError(f"axes must be axis numbers, got {axes.dtype} from {axes.min()} to {axes.max()}")
+    return axes.astype(np.uint8)
+
+
 _PACK10, _PACK4 = struct.Struct("10q").pack, struct.Struct("4q").pack  # strides, as the library reads them
 
 
@@ -415,7 +425,7 @@ def rope(q, k, positions, axes, freq, interleaved=False, inverse=False, q_out=No
         raise ValueError("k_out without k")
     if not q.numel() or (k is not None and not Hk):
         raise ValueError(f"q and k must not be empty, got {tuple(q.shape)}" + ("" if k is None else f" and {tuple(k.shape)}"))
-    axes = np.asarray(axes, dtype=np.uint8)
+    axes = _axes(axes)
     freq = np.asarray(freq, dtype=np.float64)
     if axes.ndim != 1 or axes.shape != freq.shape:
         raise ValueError(f"axes and freq must be vectors of one length, got {axes.shape} and {freq.shape}")

@@ -125,9 +125,11 @@ _ROPE_FN = None
 
 def rope(q, k, positions, axes, freq, interleaved=False, call=None):
     """eio.rope, differentiable in q and k (any number of times).  Returns (q, k) rotated.
-    `call` replaces the library call, with the signature of default_rope."""
+    May be captured into a CUDA graph, backward included, with leaves of no other autograd graph that
+    is still alive.  `call` replaces the library call, with the signature of default_rope."""
     global _ROPE_FN
     if _ROPE_FN is None:
         _ROPE_FN = _rope_function()
-    axes, freq = np.array(axes, dtype=np.uint8), np.array(freq, dtype=np.float64)  # the backward's own copy
+    from . import _axes
+    axes, freq = np.array(_axes(axes)), np.array(freq, dtype=np.float64)  # the backward's own copy
     return _ROPE_FN.apply(q, k, positions, axes, freq, interleaved, False, call or default_rope)

@@ -325,3 +325,13 @@ def test_rope_gradients_of_one_output_and_of_broadcast_inputs():
     want = ko.rope(w.numpy(), pos.numpy(), AXES, FREQ, False, -1).sum((0, 2), keepdims=True)
     np.testing.assert_allclose(base.grad, want, atol=1e-13)
     assert k.grad is None
+
+
+@pytest.mark.parametrize("axes", [[256], [-1], [0.5], np.array([256 + 1], np.int64), np.array([True])])
+def test_rope_refuses_axes_that_are_no_axis_numbers(axes):
+    q = torch.zeros(1, 3, 2, 16, dtype=torch.float64)
+    pos = torch.zeros(1, 3, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="axes"):
+        autograd.rope(q, None, pos, axes, [1.0], call=_orope)
+    for good in ([1], (1,), np.array([1], np.int32), np.array([1], np.uint8)):
+        assert autograd.rope(q, None, pos, good, [1.0], call=_orope)[0].shape == q.shape
