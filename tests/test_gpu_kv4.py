@@ -161,6 +161,32 @@ def test_rope_gradients(inter):
 
 
 # ------------------------------------------------------------------ append and read
+def test_rope_and_its_backward_in_a_graph():
+    """Both directions captured and replayed with other rows, positions and gradients give the eager results."""
+    axes, freq = _rope_table((12, 20), 3)
+
+    def step(q, k, pos, w):
+        yq, yk = autograd.rope(q, k, pos, axes, freq)
+        return yq, *torch.autograd.grad((yq * w).sum() + (yk * w[:, :, :1]).sum(), (q, k))
+    make = lambda seed: (randn((2, 6, 3, 64), seed, torch.float32).requires_grad_(),  # noqa: E731
+                         randn((2, 6, 1, 64), seed + 1, torch.float32).requires_grad_(),
+                         i32(np.random.default_rng(seed).integers(0, 900, (2, 6, 2))),
+                         randn((2, 6, 3, 64), seed + 2, torch.float32))
+    step(*make(1))
+    held = make(11)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tuple(x.detach() for x in step(*held))
+    for seed in (11, 21, 31):
+        new = make(seed)
+        with torch.no_grad():
+            for x, y in zip(held, new):
+                x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, step(*new)))
+
+
 def _table(lens, page, seed, extra=2, width=1):
     """Pages in a random order: table, the pages of each sequence, and the pool's size."""
     per = [-(-n // page) for n in lens]
