@@ -128,46 +128,59 @@ class Kv4Cache:
     def extend(self, ids, n_new):
         """Make room for n_new (a number, or one for each sequence) more tokens of each of
         the sequences; returns their Kv4Batch, the new tokens counted.  A shared page that
-        would be written is copied first.  Raises Kv4Full, with nothing changed, if the
-        pool has too few free pages."""
+        would be written is copied first.  Raises Kv4Full if the pool has too few free pages.
+        Whatever it raises, the cache is as it was before the call."""
         ids = self._ids(ids)
         counts = [int(n_new)] * len(ids) if np.ndim(n_new) == 0 else [int(n) for n in n_new]
         if len(counts) != len(ids) or min(counts) < 0:
             raise ValueError(f"n_new must be one count >= 0 for each of the {len(ids)} sequences, got {n_new}")
         seqs = [self._seq(i) for i in ids]
-        need, refs = 0, {}
+        need, refs, copies = 0, {}, []
         for s, n in zip(seqs, counts):
             need += -(-(s.length + n) // self.page) - len(s.pages)
+            shared = False
             if n and s.length % self.page:  # its last page is written
                 p = s.pages[-1]
                 refs[p] = refs.get(p, int(self._refs[p])) - 1
-                need += refs[p] >= 1
+                shared = refs[p] >= 1
+            need += shared
+            copies.append(shared)
         if need > len(self._free):
             raise Kv4Full(f"{need} pages are needed and {len(self._free)} are free")
-        src, dst = [], []
-        for s, n in zip(seqs, counts):
-            if not n:
-                continue
-            if s.length % self.page and self._refs[s.pages[-1]] > 1:
-                old, new = s.pages[-1], heapq.heappop(self._free)
-                src.append(old)
-                dst.append(new)
-                self._refs[old] -= 1
-                self._refs[new] = 1
-                s.pages[-1] = new
-            while len(s.pages) * self.page < s.length + n:
-                p = heapq.heappop(self._free)
-                self._refs[p] = 1
-                s.pages.append(p)
+        # The copies and the upload may fail: pages are only taken until both are done, then the rest changes.
+        taken = [heapq.heappop(self._free) for _ in range(need)]
+        try:
+            src, dst, tails, at = [], [], [], 0  # tails: where a sequence's new pages go in its list, and the pages
+            for s, n, shared in zip(seqs, counts, copies):
+                first = len(s.pages) - shared
+                some = taken[at:at - (-(s.length + n) // self.page) - first]
+                at += len(some)
+                if shared:
+                    src.append(s.pages[-1])
+                    dst.append(some[0])
+                tails.append((first, some))
+            self._copy(src, dst)
+            versions = [self._tick() if n else s.version for s, n in zip(seqs, counts)]
+            batch = self._batch(ids, counts, versions, tails)
+        except BaseException:
+            for p in taken:
+                heapq.heappush(self._free, p)
+            raise
+        self._refs[taken] = 1
+        for p in src:
+            self._refs[p] -= 1
+        for s, n, version, (first, some) in zip(seqs, counts, versions, tails):
+            if some:
+                s.pages[first:] = some
             s.length += n
-            s.version = self._tick()
-        self._copy(src, dst)
-        return self._batch(ids, counts)
+            s.version = version
+        return batch
 
     def batch(self, ids):
         """The Kv4Batch of sequences as they are (for read or decode)."""
         ids = self._ids(ids)
-        return self._batch(ids, [0] * len(ids))
+        seqs = [self._seq(i) for i in ids]
+        return self._batch(ids, [0] * len(ids), [s.version for s in seqs], [(len(s.pages), []) for s in seqs])
 
     def compact(self):
         """Move the pages in use to the front of the pool, so that pages pages_used() ..
@@ -194,19 +207,22 @@ class Kv4Cache:
             for layer in range(self.layers):
                 copy_pages(self.pool[layer], src, dst)
 
-    def _batch(self, ids, counts):
+    def _batch(self, ids, counts, versions, tails):
+        """The Kv4Batch of sequences with counts more tokens and with the pages `some` from
+        `first` on, as tails gives them."""
         import torch
         seqs = [self._seq(i) for i in ids]
-        B, width = len(ids), max(1, max(len(s.pages) for s in seqs))
+        B, width = len(ids), max(1, max(max(len(s.pages), first + len(some)) for s, (first, some) in zip(seqs, tails)))
         host = np.zeros(B * width + 2 * B, np.int32)  # one copy to the device: table, lengths, counts
         table = host[:B * width].reshape(B, width)
-        for b, s in enumerate(seqs):
+        for b, (s, (first, some)) in enumerate(zip(seqs, tails)):
             table[b, :len(s.pages)] = s.pages
-        host[B * width:B * width + B] = [s.length for s in seqs]
+            table[b, first:first + len(some)] = some
+        host[B * width:B * width + B] = [s.length + n for s, n in zip(seqs, counts)]
         host[B * width + B:] = counts
         dev = torch.from_numpy(host).to(self.device)
-        return Kv4Batch(ids, [s.version for s in seqs], dev[:B * width].view(B, width),
-                        dev[B * width:B * width + B], dev[B * width + B:], max(counts))
+        return Kv4Batch(ids, versions, dev[:B * width].view(B, width), dev[B * width:B * width + B],
+                        dev[B * width + B:], max(counts))
 
     def _current(self, layer, batch):
         if not 0 <= layer < self.layers:

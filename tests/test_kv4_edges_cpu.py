@@ -1,0 +1,75 @@
+"""Host side of rotary positions and the 4-bit cache where a call fails midway, where a
+tensor is not laid out as the library reads it, and where sizes pass what is counted in."""
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_sm_b200 as eio
+from exact_io_aware_sm_b200 import kv4_cache
+
+
+# ------------------------------------------------------------------ a cache whose device work fails
+def _state(cache):
+    return ({i: (list(s.pages), s.length, s.version) for i, s in cache._seqs.items()}, cache._refs.tolist(),
+            sorted(cache._free))
+
+
+def _forked(monkeypatch, layers=1):
+    """Two sequences that share a full page and a part-filled one; copies are recorded."""
+    copies = []
+    monkeypatch.setattr(eio, "copy_pages", lambda pool, src, dst, stream=None: copies.append((list(src), list(dst))))
+    cache = kv4_cache.Kv4Cache(12, 1, 64, page=16, layers=layers, device="cpu")
+    a = cache.add()
+    old = cache.extend([a], 21)
+    return cache, a, cache.fork(a), old, copies
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [16, 0], [40, 3]])
+@pytest.mark.parametrize("fails", ["first copy", "second layer's copy", "upload"])
+def test_an_extend_that_fails_leaves_the_cache_as_it_was(monkeypatch, fails, counts):
+    """A page copy or an upload that raises: no page, length, count or version has changed,
+    older batches stay valid, and the same call works once the cause is gone."""
+    cache, a, b, old, copies = _forked(monkeypatch, layers=2)
+    before, calls = _state(cache), []
+
+    def copy_pages(pool, src, dst, stream=None):
+        calls.append((list(src), list(dst)))
+        if fails != "upload" and len(calls) == (1 if fails == "first copy" else 2):
+            raise eio.AttnError(6, "a copy that fails")
+
+    def no_upload(x):
+        raise RuntimeError("out of memory")
+    with monkeypatch.context() as m:
+        m.setattr(eio, "copy_pages", copy_pages)
+        if fails == "upload":
+            m.setattr(torch, "from_numpy", no_upload)
+        with pytest.raises(RuntimeError):
+            cache.extend([a, b], counts)
+        assert calls
+    assert _state(cache) == before
+    assert cache._current(0, old) is not None
+    batch = cache.extend([a, b], counts)
+    assert copies[0] == ([1], [2]) and copies[1] == copies[0]
+    assert [cache.length(i) for i in (a, b)] == [21 + n for n in counts] == batch.seqlens.tolist()
+    for r, i in enumerate((a, b)):
+        pages = cache._seqs[i].pages
+        assert len(pages) == -(-cache.length(i) // 16) and batch.table[r, :len(pages)].tolist() == pages
+    assert cache._seqs[a].pages[1] == 2 and cache._seqs[b].pages[1] == 1
+
+
+def test_a_compaction_that_fails_leaves_the_cache_as_it_was(monkeypatch):
+    cache, a, b, old, _ = _forked(monkeypatch)
+    c = cache.add()
+    cache.extend([c], 5)
+    cache.free(a)
+    cache.free(b)
+    before = _state(cache)
+
+    def copy_pages(pool, src, dst, stream=None):
+        raise eio.AttnError(6, "a copy that fails")
+    with monkeypatch.context() as m:
+        m.setattr(eio, "copy_pages", copy_pages)
+        with pytest.raises(eio.AttnError):
+            cache.compact()
+    assert _state(cache) == before
+    assert cache.compact() == 1 and cache._seqs[c].pages == [0]
