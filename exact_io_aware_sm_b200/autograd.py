@@ -78,9 +78,10 @@ def default_rope(q, k, positions, axes, freq, interleaved, inverse):
 
 def _rows(x):
     """x, or a contiguous copy where its layout is not one that eio.rope reads (expanded
-    gradients, transposed heads, strides that are not whole 16 bytes)."""
-    if x.is_contiguous() and x.data_ptr() % 16 == 0:
-        return x
+    gradients, transposed heads, strides or addresses that are not whole 16 bytes)."""
+    import torch
+    if x.is_contiguous():
+        return x if x.data_ptr() % 16 == 0 else x.clone(memory_format=torch.contiguous_format)
     B, N, H, d = x.shape
     e = x.element_size()
     sb, sn, sh, sd = x.stride()

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import exact_io_aware_sm_b200 as eio
-from exact_io_aware_sm_b200 import kv4_cache
+from exact_io_aware_sm_b200 import autograd, kv4_cache
+from tests import kv4_oracle as ko
 
 
 # ------------------------------------------------------------------ a cache whose device work fails
@@ -73,3 +74,44 @@ def test_a_compaction_that_fails_leaves_the_cache_as_it_was(monkeypatch):
             cache.compact()
     assert _state(cache) == before
     assert cache.compact() == 1 and cache._seqs[c].pages == [0]
+
+
+# ------------------------------------------------------------------ differentiable rope
+AXES, FREQ = np.array([0, 0, 1, 1, 2], np.uint8), np.array([1.0, 0.1, 0.7, 0.02, 0.3])
+
+
+def _off_by(x, n):
+    """x's values at element n of a flat buffer: contiguous, but not on a 16-byte boundary."""
+    flat = torch.empty(n + x.numel(), dtype=x.dtype)
+    y = flat[n:].view(x.shape)
+    y.copy_(x)
+    return y
+
+
+def _orope(q, k, positions, axes, freq, interleaved, inverse):
+    """The oracle behind the library's own conditions on addresses and strides."""
+    for x in (q, k):
+        if x is not None:
+            B, N, H, d = x.shape
+            sb, sn, sh, sd = x.stride()
+            assert x.data_ptr() % 16 == 0 and sd == 1 and (H == 1 or sh == d)
+            assert all(s * x.element_size() % 16 == 0 for s, n in ((sb, B), (sn, N)) if n > 1)
+    return tuple(None if x is None else
+                 torch.from_numpy(ko.rope(x.detach().double().numpy(), positions.numpy(), axes, freq, interleaved,
+                                          -1 if inverse else 1)).to(x.dtype) for x in (q, k))
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.bfloat16, 4), (torch.bfloat16, 1), (torch.float32, 2), (torch.float64, 1)])
+def test_rope_takes_misaligned_inputs_and_gradients(dtype, n):
+    """q, k or a gradient that starts off a 16-byte boundary is copied, not refused: the same answers."""
+    g = torch.Generator().manual_seed(n)
+    q, k, dq, dk = (torch.randn(2, 3, h, 16, generator=g, dtype=torch.float64).to(dtype) for h in (2, 1, 2, 1))
+    pos = torch.randint(0, 50, (2, 3, 3), generator=g)
+
+    def both(put):
+        x, y = put(q).requires_grad_(), put(k).requires_grad_()
+        out = autograd.rope(x, y, pos, AXES, FREQ, call=_orope)
+        return [t.detach() for t in out] + list(torch.autograd.grad(out, (x, y), (put(dq), put(dk))))
+    assert _off_by(q, n).data_ptr() % 16
+    for got, want in zip(both(lambda x: _off_by(x, n)), both(torch.clone)):
+        assert torch.equal(got, want)
