@@ -106,13 +106,17 @@ def _rope_function():
         @staticmethod
         def backward(ctx, dq, dk):
             positions, = ctx.saved_tensors
+            if not ctx.needs_input_grad[0]:
+                dq = None
+            if not ctx.needs_input_grad[1]:
+                dk = None
 
             def back(x, y):
                 if torch.is_grad_enabled():  # a gradient of the gradient is wanted
                     return _Rope.apply(x, y, positions, *ctx.table, not ctx.inverse, ctx.call)
                 return ctx.call(_rows(x), None if y is None else _rows(y), positions, *ctx.table, not ctx.inverse)
 
-            if dq is None:  # only k's output was used
+            if dq is None:  # only k's output was used, or only k's gradient is wanted
                 gq, gk = None, (None if dk is None else back(dk, None)[0])
             else:
                 gq, gk = back(dq, dk)

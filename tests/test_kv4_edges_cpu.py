@@ -115,3 +115,33 @@ def test_rope_takes_misaligned_inputs_and_gradients(dtype, n):
     assert _off_by(q, n).data_ptr() % 16
     for got, want in zip(both(lambda x: _off_by(x, n)), both(torch.clone)):
         assert torch.equal(got, want)
+
+
+def test_rope_computes_only_the_gradients_that_are_wanted():
+    g = torch.Generator().manual_seed(9)
+    q, k = (torch.randn(2, 3, h, 16, generator=g, dtype=torch.float64) for h in (2, 1))
+    w = torch.randn(2, 3, 2, 16, generator=g, dtype=torch.float64)
+    pos = torch.randint(0, 50, (2, 3, 3), generator=g)
+    calls = []
+
+    def call(q, k, *rest):
+        calls.append((q is not None, k is not None))
+        return _orope(q, k, *rest)
+    want = torch.from_numpy(ko.rope(w.numpy(), pos.numpy(), AXES, FREQ, False, -1))
+    for frozen in ("k", "q", None):
+        x, y = q.clone().requires_grad_(frozen != "q"), k.clone().requires_grad_(frozen != "k")
+        yq, yk = autograd.rope(x, y, pos, AXES, FREQ, call=call)
+        calls.clear()
+        (yq * w + yk * w).sum().backward()
+        assert len(calls) == 1 and sum(calls[0]) == (1 if frozen else 2)
+        assert x.grad is None if frozen == "q" else torch.allclose(x.grad, want, atol=1e-14)
+        assert y.grad is None if frozen == "k" else torch.allclose(y.grad, want.sum(2, keepdim=True), atol=1e-13)
+    # one gradient of two leaves, and a second derivative with k frozen
+    x, y = q.clone().requires_grad_(), k.clone().requires_grad_()
+    yq, yk = autograd.rope(x, y, pos, AXES, FREQ, call=call)
+    assert torch.allclose(torch.autograd.grad((yq * w + yk * w).sum(), x)[0], want, atol=1e-14)
+    u = w.clone().requires_grad_()
+    yq, yk = autograd.rope(x, k, pos, AXES, FREQ, call=call)
+    gx, = torch.autograd.grad((yq * u + yk * u).sum(), x, create_graph=True)
+    gu, = torch.autograd.grad((gx * q).sum(), u)
+    assert torch.allclose(gu, torch.from_numpy(ko.rope(q.numpy(), pos.numpy(), AXES, FREQ, False)), atol=1e-13)
