@@ -176,6 +176,11 @@ static int check_decode(int B, int Sq, int Hq, int Hkv, int d, int n_pages, int 
   if (Hq % Hkv != 0) return fail(ATTN_ERR_SHAPE, "Hq (%d) is not a multiple of Hkv (%d)", Hq, Hkv);
   if (Sq > (1 << 20) || Hq > (1 << 20) || static_cast<double>(B) * Sq * Hq > (1 << 30))
     return fail(ATTN_ERR_SHAPE, "too many query rows");
+  // A warp counts its stages (32 keys of 8 columns; up to 4 more for a unit's rounding, start and end) in 32 bits:
+  // 2^41 are 1.4e9 for each of 148 x 11.
+  const long long blocks = (static_cast<long long>(Hq / Hkv) * Sq + 7) / 8;
+  if (static_cast<double>(B) * Hkv * blocks * ((static_cast<long long>(max_pages) << p->page_shift) / 32 + 4) >= 2199023255552.0)
+    return fail(ATTN_ERR_SHAPE, "too much work: B * Hkv * ceil(Hq / Hkv * Sq / 8) * (max_pages * page / 32 + 4) must be below 2^41");
   return ATTN_OK;
 }
 

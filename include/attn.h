@@ -429,7 +429,8 @@ int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, cons
  *   workspace  device, attn_decode_kv4_workspace() bytes; its content need not be
  *              kept or cleared.  Calls that may run at the same time need one each.
  * Any Hq % Hkv == 0 and any Sq (a KV head's (head, token) pairs go in blocks of 8, and each
- * block reads the cache).  A row that sees no token gets O = 0, LSE = -inf.  A query row that
+ * block reads the cache) with B * Sq * Hq at most 2^30 and B * Hkv * ceil(Hq / Hkv * Sq / 8) *
+ * (max_pages * page / 32 + 4) below 2^41.  A row that sees no token gets O = 0, LSE = -inf.  A query row that
  * holds an infinity, a NaN or a magnitude of 2^114 or more gives NaN.  The result does not
  * depend on timing.
  * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE; a bounded wait that

@@ -145,3 +145,27 @@ def test_rope_computes_only_the_gradients_that_are_wanted():
     gx, = torch.autograd.grad((yq * u + yk * u).sum(), x, create_graph=True)
     gu, = torch.autograd.grad((gx * q).sum(), u)
     assert torch.allclose(gu, torch.from_numpy(ko.rope(q.numpy(), pos.numpy(), AXES, FREQ, False)), atol=1e-13)
+
+
+# ------------------------------------------------------------------ sizes
+def _decode(B, Sq, Hq, H, mp, page=256, n=1 << 60):
+    fake = 0x10000  # never dereferenced: the calls fail their checks, or find no device
+    return eio.lib().attn_decode_kv4(fake, fake, fake, fake, fake, None, fake, n, B, Sq, Hq, H, 64, 8, page, mp, 0.1,
+                                     None)
+
+
+# Columns go in blocks of 8, keys in stages of 32 with three more for a block's start and end.
+@pytest.mark.parametrize("B,Sq,Hq,H,mp", [(1, 1 << 20, 1 << 10, 1, 1 << 22), (1, 1 << 20, 1, 1, 1 << 22),
+                                          (1 << 10, 1, 1 << 13, 1 << 13, 1 << 21), (1, 8, 1 << 20, 1, 1 << 18)])
+def test_decode_refuses_more_work_than_its_counts_hold(B, Sq, Hq, H, mp):
+    """A warp's stages are counted in 32 bits; pages may repeat in a table, so little memory reaches past them."""
+    assert -(-Hq // H * Sq // 8) * B * H * (mp * 8 + 3) >= 2 ** 41
+    assert _decode(B, Sq, Hq, H, mp) == 2 and "work" in eio.last_error()
+    assert eio.lib().attn_decode_kv4_workspace(B, Sq, Hq, H, 64, 256, mp) == -1
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
+@pytest.mark.parametrize("B,Sq,Hq,H,mp", [(1, 1, 32, 8, 1 << 22), (4096, 1, 64, 8, 1 << 12), (1, 4096, 64, 8, 1 << 14),
+                                          (1 << 20, 1, 8, 1, 1 << 10)])
+def test_decode_takes_large_work_that_its_counts_hold(B, Sq, Hq, H, mp):
+    assert _decode(B, Sq, Hq, H, mp) == 6  # every check passed: there is no device
