@@ -3,8 +3,9 @@
 // Pair p of a head (channels p and p + d/2, or 2p and 2p + 1) is rotated by
 //     theta = positions[b, n, axis(p)] * freq(p)
 //     (x, y) -> (x cos theta - y sin theta, x sin theta + y cos theta);
-// pairs behind the table stay as they are.  The backward is the rotation by
-// -theta.
+// pairs behind the table are copied bit by bit (a rotation by 0 would carry a partner's
+// infinity or NaN over and lose the sign of a zero, and a bf16 NaN its bits when it is
+// rounded again).  The backward is the rotation by -theta.
 //
 // Angles: theta / 2 pi modulo 1 as a 64-bit fixed-point fraction.  The host
 // turns freq into F = freq / 2 pi * 2^64 (modulo 2^64); position * F in 64-bit
@@ -81,10 +82,19 @@ __device__ __forceinline__ uint4 close_word(const float* f) {
   else return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
+// The first `live` of a word's eight bf16 values from x, the others from `old`, bit by bit.
+__device__ __forceinline__ uint4 first_of(const uint4& x, const uint4& old, int live) {
+  auto two = [&](uint32_t a, uint32_t b, int i) { return live > i + 1 ? a : live == i + 1 ? __byte_perm(a, b, 0x7610) : b; };
+  return make_uint4(two(x.x, old.x, 0), two(x.y, old.y, 2), two(x.z, old.z, 4), two(x.w, old.w, 6));
+}
+
 template <typename T>
 constexpr int kRopeEach = sizeof(T) == 2 ? 4 : 2;  // pieces of work that a thread has in flight: 128 bytes
 
-template <typename T, int D, bool INTERLEAVED>
+// PARTIAL: the table has fewer than D / 2 pairs.  A kernel of its own, since the words as they were read and
+// what tells the pairs apart cost registers: in one kernel for both, whole tables in fp32 took 95 -> 97 to 101 us
+// (613 MB).  Partial ones take 95 in fp32 and 101 to 103 in bf16 (95 and 99 when the rest was rotated by 0).
+template <typename T, int D, bool INTERLEAVED, bool PARTIAL>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kEach = kRopeEach<T>;
   constexpr int kChunks = D / 16, kHalf = D / 2;  // pieces of eight pairs, pairs of a head
@@ -97,6 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int heads = a.Hq + a.Hk, items = nt * heads * kChunks;
   const int chunk = threadIdx.x % kChunks;  // kRopeThreads is a multiple of kChunks: the same for all of a thread's items
   constexpr int V = Piece<T>::V, kWords = Piece<T>::kWords;
+  constexpr int kPairs = INTERLEAVED ? V / 2 : V;  // of a word
   Piece<T> piece[kEach];
   T* out[kEach];
   int tok[kEach];
@@ -125,8 +136,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
   for (int i = threadIdx.x; i < nt * kHalf; i += kRopeThreads) {
     const int t = i / kHalf, p = i % kHalf;
-    float s = 0.f, c = 1.f;
-    if (p < a.n_pairs) {
+    float s = 0.f, c = __uint_as_float(0x7fffffffu);  // NaN: no rotation
+    if (!PARTIAL || p < a.n_pairs) {
       int b = b0, n = n0 + t;
       while (n >= a.N) n -= a.N, ++b;
       const long long pos = a.positions[b * a.p_sb + n * a.p_sn + a.axis[p]];
@@ -157,12 +168,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           const float c = k ? r.z : r.x, s = k ? r.w : r.y;
           const int p = 2 * j + k, i = INTERLEAVED ? 2 * p : p, partner = INTERLEAVED ? i + 1 : i + 8;
           const float u = x[i], v = x[partner];
+          if (PARTIAL && sizeof(T) == 4 && c != c) continue;  // behind the table
           x[i] = u * c - v * s;
           x[partner] = u * s + v * c;
         }
       }
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) *reinterpret_cast<uint4*>(out[e] + V * (chunk + kChunks * w)) = close_word<T>(x + V * w);
+      for (int w = 0; w < kWords; ++w) {
+        uint4 y = close_word<T>(x + V * w);
+        if constexpr (PARTIAL && sizeof(T) == 2) {
+          const int pair = kPairs * (chunk + kChunks * (INTERLEAVED ? w : w % (kWords / 2)));  // the word's first
+          y = first_of(y, piece[e].word[w], (a.n_pairs - pair) * (V / kPairs));
+        }
+        *reinterpret_cast<uint4*>(out[e] + V * (chunk + kChunks * w)) = y;
+      }
     }
   }
 }
@@ -172,8 +191,9 @@ cudaError_t launch_t(bool interleaved, const RopeArgs& a, cudaStream_t s) {
   const int tokens = a.B * a.N;
   const int blocks = (tokens - 1) / a.tokens_per_block + 1;
   const size_t smem = static_cast<size_t>(a.tokens_per_block) * D / 2 * sizeof(float2);
-  if (interleaved) rope_kernel<T, D, true><<<blocks, kRopeThreads, smem, s>>>(a);
-  else rope_kernel<T, D, false><<<blocks, kRopeThreads, smem, s>>>(a);
+  auto launch = [&](auto kernel) { kernel<<<blocks, kRopeThreads, smem, s>>>(a); };
+  if (a.n_pairs < D / 2) launch(interleaved ? rope_kernel<T, D, true, true> : rope_kernel<T, D, false, true>);
+  else launch(interleaved ? rope_kernel<T, D, true, false> : rope_kernel<T, D, false, false>);
   return cudaGetLastError();
 }
 

@@ -368,7 +368,7 @@ int attn_fwd_bound(const void* q, const void* k, const void* v, void* o, float* 
  *
  * Pair p < n_pairs of every head is rotated by theta = positions[axes[p]] *
  * freq[p]: (x, y) -> (x cos - y sin, x sin + y cos).  The pair is channels p and
- * p + d / 2, or 2p and 2p + 1 (interleaved != 0); other channels are copied.
+ * p + d / 2, or 2p and 2p + 1 (interleaved != 0); other channels are copied bit by bit.
  * inverse != 0 rotates by -theta, which is also the gradient's map.  theta is
  * reduced in 64-bit fixed point: its error is below 2^-62 of itself and |position| *
  * 2^-64 turns together, whatever the position.
