@@ -26,17 +26,21 @@
 //         in as fp16, scaled by a power of two so that its largest magnitude is in
 //         [2^14, 2^15): exact down to 2^-28 of that.
 //       O^T (d x 8 columns): the scale belongs to the key, so P sv is rounded to
-//         fp16, relative to a power of two (a reference) at least as large as
-//         every scale of the group so far, as P is relative to a base that is at most 2^8
-//         below the running maximum: 2^-12 of each term down to 2^-28 of the largest.
+//         fp16, as P is relative to a base that is at most 2^8 below the column's running
+//         maximum, and as a product relative to a power of two (a reference, of a column and a
+//         group): when a reference moves, the largest product becomes 2^6 to 2^7.  2^-11 of each
+//         term, down to 2^-30 of the column's largest.  Relative to the largest scale so far,
+//         whoever sees it, a key of no weight with a V some 2^24 times larger than the others'
+//         took all their digits; this costs 1 to 3 % (64 sequences of 1024 to 8192 keys 70.7 ->
+//         71.9 us on the device, 64 query heads 79.4 -> 80.3).
 //         The codes go in as c - 8, a subtraction of subnormal numbers for two of
 //         them: taking 8 sum P sv off at the end cost a third less, but over the
 //         524287 keys the sums of c lost the digits that the difference is made of
-//         (O off by 0.0041 of its norm instead of 0.0017).
-//     The base and the references move only when a weight or a scale has outgrown
-//     them (a test of sums that are taken anyway), so that a stage needs no maximum
-//     and no shuffles (93 -> 82 us for 64 sequences of 1024 to 8192 keys, with what
-//     it made possible).
+//         (O off by 0.0041 of its norm instead of 0.0016).
+//     The base and the references of a column move only when its weights or products have
+//     outgrown them (a test of sums, and of sums of the fp16 products), so that a stage needs
+//     no maximum and no shuffles (93 -> 82 us for 64 sequences of 1024 to 8192 keys when that
+//     came in, with what it made possible).
 //     Up to 4 columns (grouped heads, one token) fill half an MMA; the other half
 //     then holds the odd groups of channels (F = 2): scaling, P sv and the sums cost
 //     half (157 -> 138 us for the 524287 keys).
@@ -65,6 +69,8 @@ constexpr int kMostIdle = 1 << 24;  // rounds (of 100 ns or so) in which no stag
 constexpr int kCombineThreads = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kMostWeight = 256.f;  // of a lane's four keys of a column, relative to the base: more moves the base
+constexpr float kMostProduct = 32768.f;  // P sv in fp16, summed over the lane's: more moves the references
+constexpr int kMostUp = 120;             // log2 of what small products are raised by (scales end at 2^-103)
 
 template <int D, int F>
 struct Cfg {
@@ -201,6 +207,14 @@ __device__ __forceinline__ uint32_t less_f16x2(uint32_t x, uint32_t y) {
 __device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {
   const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Two fp32 products in one instruction.
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -454,9 +468,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
   float acc[G][2][4];        // O^T: channels 32 group + 4 g + 2 j (and 16 times the next one), columns 2 t, 2 t + 1
   float l[2];                // sum
   float mneg[2];             // less the base (the maximum in log2 units when it last moved); inf: no key was seen yet
-  float rinv[NS];            // P sv goes in times this: 2^6 over the reference of the lane's group
-  uint32_t ref[G / 2];       // the references as bf16, packed like the scales
-  uint32_t my_ref;           // ref[t % (G / 2)]: the word that the lane checks, of row g + 8 (t / 2)
+  float rinv[NS][2];         // P sv of the lane's group goes in times this, a power of two for each column
   int seg_k0 = 0, which = 0;
 
   // The token and the query head (of the KV head's group) of a column; false where there is none.
@@ -540,10 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       l[j] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < G / 2; ++i) ref[i] = 0;
-    my_ref = 0;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) rinv[i] = pow2(106);
+    for (int i = 0; i < NS; ++i) rinv[i][0] = rinv[i][1] = pow2(kMostUp);
   };
 
   // This lane's scale of set n (its group, or the lane's one of its pair) among packed scales.
@@ -552,44 +561,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     else return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
   };
 
-
-  // The largest magnitudes of the V scales of two tiles, packed, over all rows.
-  auto largest = [&](const uint32_t (*vs)[2][G / 2], uint32_t* x) {
-#pragma unroll
-    for (int i = 0; i < G / 2; ++i) {
-      x[i] = __vmaxu2(__vmaxu2(vs[0][0][i] & 0x7fff7fffu, vs[0][1][i] & 0x7fff7fffu), __vmaxu2(vs[1][0][i] & 0x7fff7fffu, vs[1][1][i] & 0x7fff7fffu));
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) x[i] = __vmaxu2(x[i], __shfl_xor_sync(0xffffffffu, x[i], off));
-    }
-  };
-  // References that hold scales whose largest are x: 4 times those, so that they seldom move.
-  auto move_refs = [&](const uint32_t* x2) {
-#pragma unroll
-    for (int grp = 0; grp < G; ++grp) {
-      const uint32_t x = x2[grp >> 1] >> (16 * (grp & 1)) & 0xffffu, old = ref[grp >> 1] >> (16 * (grp & 1)) & 0xffffu;
-      if (x > old) {
-        const int e = min(max(static_cast<int>(x >> 7) + 3, 27), 254);  // biased exponent of the new reference
-        const bool own = F == 1 || half == (grp & 1);
-        if (old) {
-          const float down = pow2(max(static_cast<int>(old >> 7) - e, -126));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              acc[grp][0][i] *= down;
-              acc[grp][1][i] *= down;
-            }
-        }
-        if (own) rinv[grp / F] = pow2(max(6 + 127 - e, -126));
-        const uint32_t bits = static_cast<uint32_t>(e) << 7;
-        ref[grp >> 1] = grp & 1 ? (ref[grp >> 1] & 0xffffu) | bits << 16 : (ref[grp >> 1] & 0xffff0000u) | bits;
-      }
-    }
-    my_ref = t % (G / 2) ? ref[G / 2 - 1] : ref[0];
-  };
-
   // Two tiles of a stage: keys k0 .. k0 + 31; bit i of bad: the page of tile i is missing.
   auto two_tiles = [&](const uint8_t* base, int k0, int bad, int ulen) {
     float s[2][4];
-    uint32_t vs[2][2][G / 2], check[2];
+    uint32_t vs[2][2][G / 2];
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       const uint8_t* p = base + tile * C::kTile;
@@ -603,7 +578,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       const uint32_t lo = *reinterpret_cast<const uint32_t*>(p + kv4_off_ks(D) + g * (2 * G) + (t % (G / 2)) * 4);
       const uint32_t hi = *reinterpret_cast<const uint32_t*>(p + kv4_off_ks(D) + (g + 8) * (2 * G) + (t % (G / 2)) * 4);
       const uint32_t sc[4] = {lo, hi, lo, hi};
-      check[tile] = *reinterpret_cast<const uint32_t*>(p + kv4_off_vs(D) + (g + 8 * (t >> 1)) * (2 * G) + (t % (G / 2)) * 4);
       mma_bf16_first(s[tile], sc, less[0], less[1]);
       float raw[4];
 #pragma unroll
@@ -625,9 +599,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         for (int i = 0; i < 4; ++i) s[tile][i] += __shfl_xor_sync(0xffffffffu, s[tile][i], 2);
       }
     }
-    bool moves = __vmaxu2(__vmaxu2(check[0], check[1]), my_ref) != my_ref;
     if (bad || k0 + 32 > ulen - a.Sq + 1) {  // some key is past a column's last one, or its page is missing
-      moves = false;
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
@@ -635,20 +607,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           const int key = k0 + tile * 16 + 8 * r + g;
           const bool gone = (bad >> tile & 1) || key >= ulen;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < 2; ++j)
             if (gone || key >= vis[j]) s[tile][2 * r + j] = -INFINITY;
-            moves |= mneg[j] == INFINITY;
-          }
+          if (gone) {
 #pragma unroll
-          for (int i = 0; i < G / 2; ++i) {
-            if (gone) vs[tile][r][i] = 0;  // has no weight and moves no reference
-            moves |= __vmaxu2(vs[tile][r][i], ref[i]) != ref[i];
+            for (int i = 0; i < G / 2; ++i) vs[tile][r][i] = 0;
           }
         }
     }
-    // The base and the references move seldom, where weights or scales have grown too large for them: only then are
-    // the column's maximum and the largest scales looked for.
+    // P relative to the base, and P sv in fp16.  A column's base and references move seldom, where its own weights or
+    // products have grown too large for them (or are NaN: no base yet, a scale that is not finite): only then are its
+    // maximum and its largest products looked for.
     float p[2][4], some[2];
+    uint32_t pv[NS][2][2];  // [][tile][r]: the B fragments before they are transposed
+    bool moves[2];
     auto weights = [&](float n0, float n1) {
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
@@ -657,23 +629,43 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 2; ++j) some[j] = (p[0][j] + p[0][j + 2]) + (p[1][j] + p[1][j + 2]);
     };
+    auto products = [&]() {
+      __half2 sums[2][2];  // short chains: the vote waits for them
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float v = scale_at(vs[tile][r], n);
+            const float2 w = mul2(make_float2(p[tile][2 * r], p[tile][2 * r + 1]), make_float2(rinv[n][0], rinv[n][1]));
+            const float2 y = mul2(w, make_float2(v, v));  // the scale last: a weight of 0 stays 0 whatever the scale
+            pv[n][tile][r] = pack_f16x2(y.x, y.y);
+            const __half2 x = *reinterpret_cast<const __half2*>(&pv[n][tile][r]);
+            sums[tile][r] = n == 0 ? x : __hadd2(sums[tile][r], x);
+          }
+      const __half2 sum = __habs2(__hadd2(__hadd2(sums[0][0], sums[0][1]), __hadd2(sums[1][0], sums[1][1])));
+      moves[0] = !(__low2float(sum) < kMostProduct) || some[0] > kMostWeight;
+      moves[1] = !(__high2float(sum) < kMostProduct) || some[1] > kMostWeight;
+    };
     weights(mneg[0], mneg[1]);
-    moves |= some[0] > kMostWeight || some[1] > kMostWeight;
-    if (__any_sync(0xffffffffu, moves)) {
-      uint32_t most[G / 2];
-      largest(vs, most);
+    products();
+    if (__any_sync(0xffffffffu, moves[0] || moves[1])) {
+      bool mine[2];  // this lane's columns are among those that move: what one column needs changes no other
+#pragma unroll
+      for (int j = 0; j < 2; ++j) mine[j] = __ballot_sync(0xffffffffu, moves[j]) & (F == 2 ? 0x55555555u << (t & 1) : 0x11111111u << t);
       // V scales that are not finite leave the products (0 NaN = NaN would reach other groups' sums, and columns
       // that do not see the key) and go straight to the groups of the columns that see them.
-      if (__vmaxu2(most[0], most[G / 2 - 1]) != __vminu2(__vmaxu2(most[0], most[G / 2 - 1]), 0x7f7f7f7fu)) {
-        uint32_t odd = 0;
+      uint32_t odd = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-          for (int i = 0; i < G / 2; ++i) {
-            uint32_t& v = vs[x >> 1][x & 1][i];
-            if ((v & 0x7f80u) == 0x7f80u) odd |= 1u << (x * 8 + 2 * i), v &= 0xffff0000u;
-            if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (x * 8 + 2 * i), v &= 0xffffu;
-          }
+        for (int i = 0; i < G / 2; ++i) {
+          uint32_t& v = vs[x >> 1][x & 1][i];
+          if ((v & 0x7f80u) == 0x7f80u) odd |= 1u << (x * 8 + 2 * i), v &= 0xffff0000u;
+          if ((v & 0x7f800000u) == 0x7f800000u) odd |= 2u << (x * 8 + 2 * i), v &= 0xffffu;
+        }
+      if (__any_sync(0xffffffffu, odd != 0)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t sees = 0;
@@ -688,9 +680,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
               for (int i = 0; i < 2; ++i) acc[grp][i][j] = acc[grp][i][j + 2] = __uint_as_float(0x7fffffffu);
             }
         }
-        largest(vs, most);
       }
-      move_refs(most);
+      float alpha[2];  // what a new base leaves of the column's sums
+      int up[2];       // the octaves of it; differences of whole numbers, so that many moves lose one at most
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float v = fmaxf(fmaxf(s[0][j], s[0][j + 2]), fmaxf(s[1][j], s[1][j + 2]));
@@ -698,23 +690,46 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
         v *= fac[j];
-        if (v > -mneg[j]) {
+        alpha[j] = 1.f;
+        up[j] = 0;
+        if (mine[j] && v > -mneg[j]) {
           if (mneg[j] != INFINITY) {
-            const float alpha = wm_ex2(-mneg[j] - v);
-            l[j] *= alpha;
-#pragma unroll
-            for (int grp = 0; grp < G; ++grp)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                acc[grp][i][j] *= alpha;
-                acc[grp][i][j + 2] *= alpha;
-              }
+            alpha[j] = wm_ex2(-mneg[j] - v);
+            up[j] = static_cast<int>(fminf(floorf(v) - floorf(-mneg[j]), 126.f));
+            l[j] *= alpha[j];
           }
           mneg[j] = -v;
         }
       }
       // a column that still sees no key has weights 0
       weights(mneg[0] == INFINITY ? 0.f : mneg[0], mneg[1] == INFINITY ? 0.f : mneg[1]);
+      // The largest product of the stage becomes 2^6 to 2^7, or less where an earlier one is larger.
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = 0.f;
+#pragma unroll
+          for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) x = fmaxf(x, fabsf(p[tile][2 * r + j] * scale_at(vs[tile][r], n)));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+          if (mine[j]) {
+            const int old = static_cast<int>(__float_as_uint(rinv[n][j]) >> 23) - 127;
+            const int now = min(min(old + up[j], 6 + 127 - static_cast<int>(__float_as_uint(x) >> 23)), kMostUp);
+            const float f = alpha[j] * pow2(max(now - old, -126));
+            rinv[n][j] = pow2(now);
+#pragma unroll
+            for (int grp = n * F; grp < n * F + F; ++grp)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                acc[grp][i][j] *= f;
+                acc[grp][i][j + 2] *= f;
+              }
+          }
+        }
+      products();
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) l[j] += some[j];
@@ -726,9 +741,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       for (int r = 0; r < 2; ++r) lds_words<G>(at + kv4_off_v(D) + ((r * 8 + g) * 4 + t) * (4 * G), w[r]);
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
-        const float v_lo = scale_at(vs[tile][0], n) * rinv[n], v_hi = scale_at(vs[tile][1], n) * rinv[n];
-        const uint32_t b0 = transposed(pack_f16x2(p[tile][0] * v_lo, p[tile][1] * v_lo));
-        const uint32_t b1 = transposed(pack_f16x2(p[tile][2] * v_hi, p[tile][3] * v_hi));
+        const uint32_t b0 = transposed(pv[n][tile][0]), b1 = transposed(pv[n][tile][1]);
 #pragma unroll
         for (int grp = n * F; grp < n * F + F; ++grp) {
           // c - 8 in rows g and 16 (c - 8) in rows g + 8, from c, 16 c, and c + 16 c' with 128 + c: all exact
@@ -764,13 +777,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
         float* part = slot + c * D + 4 * g + 32 * half;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          // 1 / rinv, exactly; raw numerators are in units of 2^-24 (odd channels: of 2^-20)
-          const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n])) * inv;
+          // raw numerators are in units of 2^-24 (odd channels: of 2^-20); 1 / rinv is exact, and goes in last
+          const float f = __uint_as_float((254u << 23) - __float_as_uint(rinv[n][j]));
           float y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = j + 2 * (i & 1);
-            y[i] = (half ? acc[F * n + F - 1][i >> 1][at] : acc[F * n][i >> 1][at]) * (i & 1 ? pow2(20) : pow2(24)) * f;
+            y[i] = (half ? acc[F * n + F - 1][i >> 1][at] : acc[F * n][i >> 1][at]) * inv * (i & 1 ? pow2(20) : pow2(24)) * f;
           }
           if (whole) *reinterpret_cast<uint2*>(o + 32 * F * n) = make_uint2(wm_pack_bf16x2(y[0], y[1]), wm_pack_bf16x2(y[2], y[3]));
           else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);

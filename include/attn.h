@@ -423,7 +423,10 @@ int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, cons
  * attn_decode_kv4 -- attn_decode_multi over the 4-bit paged cache.
  *
  * The last Sq tokens of each sequence are the queries; token s attends to tokens
- * 0 .. seqlens[b] - Sq + s.  K and V are (c - 8) s exactly (not rounded to bf16).
+ * 0 .. seqlens[b] - Sq + s.  K and V are (c - 8) s exactly (not rounded to bf16).  In the sum
+ * with V a weight times a group's scale is a number of 11 bits (fp16): 2^-11 of each term, down
+ * to 2^-30 of the largest that the row has in that group.  Tokens that a row does not see do not
+ * change its result.
  *   q    device, [B, Sq, Hq, d] bf16; o  device, the same (written)
  *   lse  device, fp32 [B, Hq, Sq] (written); may be NULL
  *   workspace  device, attn_decode_kv4_workspace() bytes; its content need not be
