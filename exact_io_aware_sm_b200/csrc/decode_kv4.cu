@@ -67,6 +67,7 @@ constexpr int kUnitCost = 3;  // of a unit's start and end, in stages (measured:
 constexpr int kRingBudget = 222 * 1024;
 constexpr int kMostIdle = 1 << 24;  // rounds (of 100 ns or so) in which no stage was taken
 constexpr int kCombineThreads = 512;
+constexpr float kSpare = 12.f;  // a join's weights are 2^-12 at most, so that numerators up to fp32's largest add up within it
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kMostWeight = 256.f;  // of a lane's four keys of a column, relative to the base: more moves the base
 constexpr float kMostProduct = 32768.f;  // P sv in fp16, summed over the lane's: more moves the references
@@ -772,7 +773,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       int hd, tk;
       if (column(2 * t + j, c0, &hd, &tk)) {
         const int c = (2 * t + j) & (C::kCols - 1);
-        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        // A part of a unit leaves its sums times the power of two that makes the sum of P 1/2 to 1: its numerators
+        // are then no larger than V.
+        const int e = min(max(static_cast<int>(__float_as_uint(sum) >> 23) - 126, -126), 126);
+        const float inv = sum == 0.f ? 0.f : whole ? 1.f / sum : pow2(-e);
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (row0 + static_cast<size_t>(tk) * a.Hq + hd) * D + 4 * g + 32 * half;
         float* part = slot + c * D + 4 * g + 32 * half;
 #pragma unroll
@@ -789,7 +793,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
           else *reinterpret_cast<float4*>(part + 32 * F * n) = make_float4(y[0], y[1], y[2], y[3]);
         }
         if (g == 0 && half == 0) {
-          if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(-mneg[j], sum);
+          if (!whole) *reinterpret_cast<float2*>(slot + C::kCols * D + 2 * c) = make_float2(e - mneg[j], sum * inv);
           else if (a.lse) a.lse[(static_cast<size_t>(ub) * a.Hq + uh * heads + hd) * a.Sq + tk] = sum == 0.f ? -INFINITY : (log2f(sum) - mneg[j]) * kLn2;
         }
       }
@@ -871,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       }
       float top = M;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x + kSpare);
       const float zero = top == -INFINITY ? 0.f : top, old = wm_ex2(M - zero);
       M = top;
       sum *= old;
@@ -929,7 +933,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_kv4_combine_kernel(con
       const float* from = slots + (static_cast<size_t>(i - 1 + k) * C::kSlots + C::W + (k == 0 ? late : 0)) * C::kSlotFloats;
       const float2 ml = *reinterpret_cast<const float2*>(from + C::kCols * D + 2 * c);
       const float4 v = *reinterpret_cast<const float4*>(from + c * D + ch);
-      const float top = fmaxf(M, ml.x), zero = top == -INFINITY ? 0.f : top;
+      const float top = fmaxf(M, ml.x + kSpare), zero = top == -INFINITY ? 0.f : top;
       const float old = wm_ex2(M - zero), wt = wm_ex2(ml.x - zero);
       M = top;
       sum = fmaf(wt, ml.y, sum * old);

@@ -225,6 +225,20 @@ def test_decode_of_values_that_change_size_along_the_keys(what, B, L, H, d, G):
     _check(o, lse, q, k, v, 1 / math.sqrt(d))
 
 
+@pytest.mark.parametrize("d,G", FORMS)
+@pytest.mark.parametrize("B,L,H", RUNS)
+def test_decode_of_values_near_the_types_largest(B, L, H, d, G):
+    """Every V about 3e38, with weights that add up past it before they are divided by their sum."""
+    q, k, v = _inputs(B, L, H, G, 3, d, 7)
+    v = torch.where(v < 0, -3.0e38, 3.0e38) * (1 - 0.2 * v.abs().clamp(max=1))
+    q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+    pool, table, n = _filled(k, v, B, 16)
+    o, lse = eio.attn_decode_kv4(q, pool, table, n)
+    eio.sync_status()
+    assert torch.isfinite(o.float()).all()
+    _check(o, lse, q, k, v, 1 / math.sqrt(d))
+
+
 @pytest.mark.parametrize("G", [4, 8])
 def test_decode_keeps_its_digits_over_half_a_million_keys(G):
     """The norm of O's error over O's.  The weights are flat, so that O is a mean of n values, sqrt(n) times
