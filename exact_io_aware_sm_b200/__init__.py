@@ -512,7 +512,8 @@ def kv4_append(k, v, pool, table, seqlens, n_new=None, stream=None):
     """Quantise k, v [B,N,Hkv,d] bf16 (any batch and token strides of whole 16 bytes) and
     write them into the pages of pool (kv4_pool) that table int32 [B,max_pages] names, as
     tokens seqlens[b] - n_new[b] .. seqlens[b] - 1; n_new int32 [B] (None: N each), rows
-    behind it are padding.  Nothing else in the pool changes.  Returns pool."""
+    behind it are padding.  Nothing else in the pool changes.  The page size follows from the
+    pool's bytes and d, so d has to be the pool's (Kv4Cache checks it).  Returns pool."""
     import torch
     if stream is not None:
         with _on(stream):

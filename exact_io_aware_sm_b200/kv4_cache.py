@@ -231,11 +231,16 @@ class Kv4Cache:
             raise ValueError("a sequence of this batch was extended, truncated, freed or moved after the batch was made")
         return self.pool[layer]
 
+    def _same_d(self, x, name):
+        if x.dim() != 4 or x.shape[3] != self.d:  # the pool's bytes alone would take 64 for 128 and half the page
+            raise ValueError(f"{name} has shape {tuple(x.shape)}; the cache holds heads of d = {self.d}")
+
     def append(self, layer, k, v, batch):
         """Write k, v [B,N,Hkv,d] bf16, row b's first n_new[b] tokens (the rest is padding),
         as the newest tokens of the batch's sequences."""
         from . import kv4_append
         pool = self._current(layer, batch)
+        self._same_d(k, "k")
         if k.shape[1] < batch.most_new:
             raise ValueError(f"k has {k.shape[1]} rows a sequence; the batch has up to {batch.most_new} new tokens")
         kv4_append(k, v, pool, batch.table, batch.seqlens, n_new=batch.n_new)
@@ -248,5 +253,6 @@ class Kv4Cache:
     def decode(self, layer, q, batch, scale=None, want_lse=True):
         """Attention of the newest Sq tokens, q [B,Sq,Hq,d], over the batch's sequences."""
         from . import attn_decode_kv4
-        return attn_decode_kv4(q, self._current(layer, batch), batch.table, batch.seqlens, scale=scale,
-                               want_lse=want_lse)
+        pool = self._current(layer, batch)
+        self._same_d(q, "q")
+        return attn_decode_kv4(q, pool, batch.table, batch.seqlens, scale=scale, want_lse=want_lse)

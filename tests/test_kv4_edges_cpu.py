@@ -169,3 +169,27 @@ def test_decode_refuses_more_work_than_its_counts_hold(B, Sq, Hq, H, mp):
                                           (1 << 20, 1, 8, 1, 1 << 10)])
 def test_decode_takes_large_work_that_its_counts_hold(B, Sq, Hq, H, mp):
     assert _decode(B, Sq, Hq, H, mp) == 6  # every check passed: there is no device
+
+
+# ------------------------------------------------------------------ a cache and rows of another head size
+def test_cache_refuses_rows_and_queries_of_another_head_size(monkeypatch):
+    """A page of 64 tokens of 128 channels has as many bytes as one of 128 tokens of 64: the pool alone does not
+    tell them apart, the cache does."""
+    assert eio.kv4_page_bytes(64, 1, 128) == eio.kv4_page_bytes(128, 1, 64)
+    called = []
+    for name in ("kv4_append", "attn_decode_kv4"):
+        monkeypatch.setattr(eio, name, lambda *a, **kw: called.append(a))
+    cache = kv4_cache.Kv4Cache(4, 2, 128, page=64, device="cpu")
+    a = cache.add()
+    batch = cache.extend([a], 3)
+    for d in (64, 32):
+        k = torch.zeros(1, 3, 2, d, dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match="d = 128"):
+            cache.append(0, k, k, batch)
+        with pytest.raises(ValueError, match="d = 128"):
+            cache.decode(0, k[:, :1], batch)
+    assert not called
+    k = torch.zeros(1, 3, 2, 128, dtype=torch.bfloat16)
+    cache.append(0, k, k, batch)
+    cache.decode(0, k[:, :1], batch)
+    assert len(called) == 2
