@@ -54,9 +54,9 @@ class Kv4Cache:
         if n_pages < 1 or layers < 1:
             raise ValueError(f"n_pages and layers must be >= 1, got {n_pages} and {layers}")
         self.n_pages, self.Hkv, self.d, self.page, self.layers = n_pages, Hkv, d, page, layers
-        self.device = torch.device("cuda" if device is None else device)
         self.pool = torch.empty((layers, n_pages, Hkv, kv4_page_bytes(page, 1, d)), dtype=torch.uint8,
-                                device=self.device)
+                                device="cuda" if device is None else device)
+        self.device = self.pool.device  # with its number: tables go where the pool is, whatever device is current
         self._refs = np.zeros(n_pages, np.int64)
         self._free = list(range(n_pages))  # a heap: the lowest page first
         self._seqs = {}

@@ -24,6 +24,7 @@ import torch
 
 import exact_io_aware_sm_b200 as eio
 from exact_io_aware_sm_b200 import autograd
+from exact_io_aware_sm_b200.kv4_cache import Kv4Cache
 from tests import kv4_oracle as ko
 
 pytestmark = pytest.mark.gpu
@@ -92,6 +93,16 @@ def test_rope_takes_gradients_off_a_16_byte_boundary(dtype, off):
     y, _ = autograd.rope(q, None, pos, [0] * 32, 100.0 ** (-np.arange(32) / 32))
     want, = torch.autograd.grad(y, q, dq, retain_graph=True)
     assert other.data_ptr() % 16 and torch.equal(torch.autograd.grad(y, q, other)[0], want)
+
+
+# ------------------------------------------------------------------ cache
+@pytest.mark.parametrize("device", [None, "cuda", "cuda:0", torch.device("cuda")])
+def test_a_cache_stays_on_the_device_that_it_was_made_on(device):
+    """Its device has a number: "cuda" alone would send a later table to whatever device is current then."""
+    cache = Kv4Cache(4, 1, 64, device=device)
+    assert cache.device == cache.pool.device and cache.device.index == torch.cuda.current_device()
+    batch = cache.extend([cache.add()], 5)
+    assert batch.table.device == batch.seqlens.device == cache.pool.device
 
 
 # ------------------------------------------------------------------ decode
