@@ -4,10 +4,12 @@
 //     O = softmax(q K^T scale) V,   K = (ck - 8) sk,  V = (cv - 8) sv
 //
 // The cache is read once: 18 d / 8 bits of codes and scales a key and KV head.
-// What bounds the kernel beside HBM is the integer pipe, which takes two cycles an
-// instruction: 0.5 of them a value to widen the codes.  524287 keys x 8 KV heads (604
-// MB) take 114 to 123 us, 4.9 to 5.3 TB/s of the 6.46 that a copy reaches; the loads
-// alone (a build without the arithmetic) took 101.
+// 524287 keys x 8 KV heads (604 MB) take 111 us while the clock holds and 124 when the load
+// has brought it down, 5.4 to 4.9 TB/s of the 6.46 that a copy reaches.  At 1.78 GHz that is 202
+// thousand cycles, of which HBM's rate accounts for 166 and the start and the joining for about 20.  The
+// 264 instructions of 16 keys (45 % of them integer ones, which take two cycles each) need about 340
+// cycles of a scheduler, HBM's rate gives it 376 at 1.78 GHz and 342 at 1.62: the lower the clock, the more
+// the instructions bind.  64 sequences of 1024 to 8192 keys (333 MB): 72 us.
 //
 //   decode_kv4_kernel  persistent, one CTA per SM.  A stage is 32 keys (two
 //     tiles of the cache) of a unit (sequence, KV head, block of at most 8

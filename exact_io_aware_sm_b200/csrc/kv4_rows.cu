@@ -12,11 +12,12 @@
 // the other token.  A token's bytes are its own: a tile that is covered in part
 // is written in part, never read.
 //
-// Both are memory bound: per token and head 4 d bytes of bf16 rows and d + d / 8
-// bytes of cache.  Narrowing is bound by the integer pipe as well (about 9 instructions a
-// value with the group's maximum and scale).  16384 tokens of 8 heads of 128 (86 MB each
-// way, 13.3 us at the rate of a copy): append 19.1 us, read 15.4; a thread a group of 32
-// channels, with its scattered stores, took 58 for both.
+// Both move, per token and head, 4 d bytes of bf16 rows and d + d / 8 bytes of cache.
+// 16384 tokens of 8 heads of 128 (86 MB each way, 13.3 us at the rate of a copy): append
+// 18.5 us, read 15.4; a thread a group of 32 channels, with its scattered stores, took 58
+// for both.  The append fills no pipe (9 instructions a value; the integer pipe is busy for
+// 53 % of the cycles, issue slots 55 %): its blocks make 2.3 rounds of 6 an SM, each of
+// which loads, narrows and stores once, so that the rounds' loads and arithmetic hardly overlap.
 #include <cuda_bf16.h>
 
 #include "kernels_kv4.h"

@@ -11,8 +11,8 @@
 // turns freq into F = freq / 2 pi * 2^64 (modulo 2^64); position * F in 64-bit
 // integers is then reduced exactly, with an error below |position| * 2^-64
 // turns, however far the position; its upper 32 bits, as a signed fraction of
-// a half turn, go to sincospif.  In fp32 the product alone would be off by
-// 2^-24 of its size: 0.06 rad at a position of a million.
+// a half turn rounded to fp32 (pi 2^-25 = 2^-23.3 rad), go to sincospif.  In fp32 the product
+// alone would be off by 2^-24 of its size: 0.06 rad at a position of a million.
 //
 // Memory bound: q and k are read and written once.  A block takes a run of
 // tokens; it computes the cosines and sines of its (token, pair)s once into

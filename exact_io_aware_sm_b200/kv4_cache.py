@@ -85,7 +85,9 @@ class Kv4Cache:
         return i
 
     def fork(self, i):
-        """A new sequence with the tokens of sequence i, in the same pages."""
+        """A new sequence with the tokens of sequence i, in the same pages.  Rows that extend has
+        counted but append has not written yet reach both only if they are appended (in every
+        layer) before either is extended, which copies a part-filled page as it is."""
         s = self._seq(i)
         for p in s.pages:
             self._refs[p] += 1

@@ -370,8 +370,8 @@ int attn_fwd_bound(const void* q, const void* k, const void* v, void* o, float* 
  * freq[p]: (x, y) -> (x cos - y sin, x sin + y cos).  The pair is channels p and
  * p + d / 2, or 2p and 2p + 1 (interleaved != 0); other channels are copied bit by bit.
  * inverse != 0 rotates by -theta, which is also the gradient's map.  theta is
- * reduced in 64-bit fixed point: its error is below 2^-62 of itself and |position| *
- * 2^-64 turns together, whatever the position.
+ * reduced to a turn in 64-bit fixed point and rounded to fp32 after that: it is off
+ * by less than 2^-23 rad, and 2^-62 of its own size, at any position.
  *   q, q_out   device, [B, N, Hq, d] (dtype); k, k_out  device, [B, N, Hk, d], Hk may be 0
  *              q_out may be q (k_out may be k) with the same strides
  *   positions  device, int32 [B, N, n_axes], the last dimension contiguous
@@ -425,17 +425,17 @@ int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, cons
  * The last Sq tokens of each sequence are the queries; token s attends to tokens
  * 0 .. seqlens[b] - Sq + s.  K and V are (c - 8) s exactly (not rounded to bf16).  In the sum
  * with V a weight times a group's scale is a number of 11 bits (fp16): 2^-11 of each term, down
- * to 2^-30 of the largest that the row has in that group.  Tokens that a row does not see do not
- * change its result.
+ * to 2^-30 of the largest that the row has in that group; a query's channels are exact, or within
+ * 2^-35 of the row's largest.  Tokens that a row does not see do not change its result.
  *   q    device, [B, Sq, Hq, d] bf16; o  device, the same (written)
  *   lse  device, fp32 [B, Hq, Sq] (written); may be NULL
  *   workspace  device, attn_decode_kv4_workspace() bytes; its content need not be
  *              kept or cleared.  Calls that may run at the same time need one each.
  * Any Hq % Hkv == 0 and any Sq (a KV head's (head, token) pairs go in blocks of 8, and each
  * block reads the cache) with B * Sq * Hq at most 2^30 and B * Hkv * ceil(Hq / Hkv * Sq / 8) *
- * (max_pages * page / 32 + 4) below 2^41.  A row that sees no token gets O = 0, LSE = -inf.  A query row that
- * holds an infinity, a NaN or a magnitude of 2^114 or more gives NaN.  The result does not
- * depend on timing.
+ * (max_pages * page / 32 + 4) below 2^41.  A row that sees no token gets O = 0, LSE = -inf.
+ * A query row that holds an infinity, a NaN or a magnitude of 2^114 or more gives NaN.  The
+ * result does not depend on timing.
  * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE; a bounded wait that
  * runs out latches ATTN_ERR_DEVICE_TIMEOUT.
  */

@@ -193,3 +193,19 @@ def test_cache_refuses_rows_and_queries_of_another_head_size(monkeypatch):
     cache.append(0, k, k, batch)
     cache.decode(0, k[:, :1], batch)
     assert len(called) == 2
+
+
+@pytest.mark.parametrize("d,columns,MB", [(64, 4, 2.7), (64, 8, 5.3), (128, 4, 5.2), (128, 8, 8.0)])
+def test_decode_workspace_sizes(d, columns, MB):
+    """149 starts of runs, and for each of 148 CTAs a slot a warp (15, or 11 where 8 columns of 128 channels need the
+    registers) and two that leave it: fp32 numerators, a maximum and a sum a column.  Longer contexts need no more."""
+    size = eio.lib().attn_decode_kv4_workspace
+    warps = 11 if columns == 8 and d == 128 else 15
+    slot = columns * (d + 2) * 4
+    want = 149 * 32 + 148 * (warps + 2) * slot
+    assert round(want / 1e6, 1) == MB
+    for G, Sq in ((columns, 1), (columns // 4, 4), (2 * columns - 1 if columns == 8 else columns, 1)):
+        for B, H, mp in ((64, 8, 128), (1, 8, 8192), (1, 1, 1 << 24)):
+            assert size(B, Sq, G * H, H, d, 64, mp) == want
+    # fewer stages of 32 keys than SMs: as many CTAs
+    assert size(1, 1, columns, 1, d, 16, 3) == 149 * 32 + 2 * (warps + 2) * slot
