@@ -33,7 +33,7 @@
 //         group): when a reference moves, the largest product becomes 2^6 to 2^7.  2^-11 of each
 //         term, down to 2^-30 of the column's largest.  Relative to the largest scale so far,
 //         whoever sees it, a key of no weight with a V some 2^24 times larger than the others'
-//         took all their digits; this costs 1 to 3 % (64 sequences of 1024 to 8192 keys 70.7 ->
+//         took all their digits; this costs 1 to 5 % (64 sequences of 1024 to 8192 keys 70.7 ->
 //         71.9 us on the device, 64 query heads 79.4 -> 80.3).
 //         The codes go in as c - 8, a subtraction of subnormal numbers for two of
 //         them: taking 8 sum P sv off at the end cost a third less, but over the
@@ -500,6 +500,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const int e = min(max(141 - static_cast<int>(mx >> 7), -100), 100);  // q 2^e
+    // A row that is not finite, or would not be as fp16, gives NaN by its sum; its scores would be NaN at every stage.
+    const uint32_t none = mx >> 7 > 242 ? 0x7fffffffu : 0u;
+    if (none) {
+#pragma unroll
+      for (int grp = 0; grp < G; ++grp) raw[grp] = make_uint4(0u, 0u, 0u, 0u);
+    }
     // Positive and finite, so that masked scores (-inf) and scores of 0 stay what they are whatever the scale.
     const float fc = fminf(fmaxf(a.scale_log2 * pow2(24 - e), pow2(-126)), 3.0e38f);
     // Codes n and n + 4 of a word sit 16 bits apart; odd n are masked 4 bits higher, 16 times as large.
@@ -552,7 +558,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1)
       column(2 * t + j, c0, &hd, &tk);
       vis[j] = ulen - a.Sq + 1 + tk;
       mneg[j] = INFINITY;
-      l[j] = 0.f;
+      const uint32_t sum = __shfl_sync(0xffffffffu, none, (2 * t + j) * 4);
+      l[j] = vis[j] > 0 ? __uint_as_float(sum) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) rinv[i][0] = rinv[i][1] = pow2(kMostUp);

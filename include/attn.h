@@ -434,7 +434,7 @@ int attn_kv4_read(void* k, void* v, const void* pool, const int32_t* table, cons
  * Any Hq % Hkv == 0 and any Sq (a KV head's (head, token) pairs go in blocks of 8, and each
  * block reads the cache) with B * Sq * Hq at most 2^30 and B * Hkv * ceil(Hq / Hkv * Sq / 8) *
  * (max_pages * page / 32 + 4) below 2^41.  A row that sees no token gets O = 0, LSE = -inf.
- * A query row that holds an infinity, a NaN or a magnitude of 2^114 or more gives NaN.  The
+ * Another that holds an infinity, a NaN or a magnitude of 2^116 or more gives NaN.  The
  * result does not depend on timing.
  * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, CUDA, WORKSPACE; a bounded wait that
  * runs out latches ATTN_ERR_DEVICE_TIMEOUT.

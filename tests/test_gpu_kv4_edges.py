@@ -277,3 +277,32 @@ def test_decode_keeps_its_digits_over_half_a_million_keys(G):
     assert (lse[0, :, 0].double() - lref).abs().max() <= 1e-4
     err = (o[0, 0].double() - ref).norm() / ref.norm()
     assert err <= 2.0 ** -9, float(err)
+
+
+@pytest.mark.parametrize("d,G", FORMS)
+@pytest.mark.parametrize("B,L,H", [(1, 500, 2), (300, 150, 4), (40, 2, 3)])
+def test_decode_of_query_rows_that_are_not_finite(B, L, H, d, G):
+    """Such rows are NaN, O and LSE, if they see a token, and 0 and -inf if not; the others are what they are
+    without them, bit for bit.  2^115.9 is a size like any other, 2^116 is not."""
+    q, k, v = (x.to(torch.bfloat16) for x in _inputs(B, L, H, G, 3, d, 9))
+    pool, table, n = _filled(k, v, B)
+    want, lse = eio.attn_decode_kv4(q, pool, table, n)
+    q2 = q.clone()
+    bad = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    for i, x in enumerate((math.nan, math.inf, -math.inf, 2.0 ** 116, -3.0e38)):
+        h = (i * 7) % (G * H)
+        q2[i % B, :, h, (5 + 40 * i) % d] = x
+        bad[i % B, :, h] = True
+    o, l = eio.attn_decode_kv4(q2, pool, table, n)
+    sees = (L - 3 + 1 + torch.arange(3, device="cuda") > 0)[None, :, None] & torch.ones_like(bad)
+    assert sees.all() == (L > 2)
+    assert torch.equal(torch.isnan(o), (bad & sees)[..., None].expand_as(o))
+    assert torch.equal(torch.isnan(l), (bad & sees).transpose(1, 2))
+    assert torch.equal(o[~bad], want[~bad]) and torch.equal(l.transpose(1, 2)[~bad], lse.transpose(1, 2)[~bad])
+    assert (o[~sees] == 0).all() and (l.transpose(1, 2)[~sees] == -math.inf).all()
+    q2 = torch.zeros_like(q)
+    q2[..., 3] = 2.0 ** 115.9
+    o, l = eio.attn_decode_kv4(q2, pool, table, n, scale=2.0 ** -118)
+    eio.sync_status()
+    if L > 2:
+        _check(o, l, q2, k, v, 2.0 ** -118)
